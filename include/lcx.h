@@ -63,7 +63,8 @@ typedef enum {
     LCX_ERR_INVALID_ARG = 1,
     LCX_ERR_UNSUPPORTED = 2,
     LCX_ERR_CUDA = 3,
-    LCX_ERR_TIMEOUT = 4
+    LCX_ERR_TIMEOUT = 4,
+    LCX_ERR_NO_PAGES = 5    /* device status word only: a page cache ran out of pages */
 } lcx_status;
 
 /* Frequency-scaling modes ([LC] 2.3, 4.2, 5.2, 6.2, 7.3; [B83] 8.3.2-8.3.3).
@@ -365,6 +366,238 @@ LCX_API lcx_status lcx_attn_merge(const float *o_parts, const float *lse_parts, 
  */
 LCX_API lcx_status lcx_attn_fwd_split_static(const lcx_attn_args *args, int32_t num_splits,
                                              void *stream);
+
+/* ------------------------------------------------------------------ page cache
+ * A key/value cache in pages of page_size tokens, for sequences that grow,
+ * share a prefix and end at different times.  Page p of layer x holds
+ * page_size slots of Hkv heads of D values in k_pages and in v_pages; the
+ * token at position j of sequence s lies in page block_table[s][j / page_size],
+ * slot j % page_size.  Keys are stored rotated (lcx_paged_append), mscale
+ * included.  The caller owns every buffer; the bookkeeping is int32 device
+ * memory that the lcx_pages_* calls keep consistent:
+ *   block_table [max_seqs, max_pages]  page numbers; -1 where there is none
+ *   seq_lens    [max_seqs]             tokens in the cache
+ *   ref_counts  [num_pages]            sequences that hold the page; 0 = free
+ *   free_pages  [num_pages]            stack of free pages: the first *n_free
+ *                                      entries, the others -1
+ *   n_free      [1]
+ *   scratch     [lcx_paged_scratch_ints(num_pages)]  zero before the first call
+ * An empty cache: block_table -1, seq_lens 0, ref_counts 0, free_pages[i] =
+ * num_pages - 1 - i, *n_free = num_pages, scratch 0.  Calls that change one
+ * cache must be ordered (one stream, or events between streams).  A sequence's
+ * last page is shared with no other sequence unless it is full, so appending
+ * never writes into a shared page.  Device-side checks: a page number outside
+ * [0, num_pages) is never followed (its keys count as hidden), and such an
+ * entry, a bad sequence number or a lack of pages is reported through the
+ * optional dev_status word (written, never cleared) with the entry skipped.
+ */
+typedef struct {
+    void *k_pages, *v_pages;   /* DEVICE [num_layers, num_pages, page_size, Hkv, D]   */
+    int32_t *block_table, *seq_lens, *ref_counts, *free_pages, *n_free, *scratch; /* DEVICE */
+    int32_t dtype;             /* lcx_dtype of both pools                             */
+    int32_t page_size;         /* a power of two, 1..1024                             */
+    int64_t num_layers, num_pages, Hkv, D, max_seqs, max_pages;
+    int64_t k_strides[5], v_strides[5]; /* elements, per (layer, page, slot, head, dim);
+                                  dim's is 1, the others multiples of 16 bytes        */
+} lcx_paged_cache;
+
+/* Most entries of one lcx_pages_* call. */
+#define LCX_PAGES_MAX_ENTRIES 1024
+
+/* int32 values of lcx_paged_cache.scratch (-1: num_pages out of range). */
+LCX_API int64_t lcx_paged_scratch_ints(int64_t num_pages);
+
+/*
+ * lcx_pages_extend -- room for new tokens: sequence seq_ids[i] grows by
+ * n_new[i] tokens (by one each when n_new is NULL), pages taken from the top
+ * of the free stack.
+ *   seq_ids, n_new, start : DEVICE int32 [n].  start[i] receives the position
+ *   of the first new token (the old length), or -1 for a skipped entry.
+ *   Skipped: a negative seq_id (a padded entry); with a status: a seq_id >=
+ *   max_seqs or seen earlier in the call, a negative n_new, a length beyond
+ *   max_pages * page_size (LCX_ERR_INVALID_ARG); entries from the first one on
+ *   whose pages, counted in order, exceed the free ones (LCX_ERR_NO_PAGES).
+ *   The granted entries take the topmost pages of the stack as one block, the
+ *   first entry from its lowest place.
+ */
+LCX_API lcx_status lcx_pages_extend(const lcx_paged_cache *cache, const int32_t *seq_ids,
+                                    const int32_t *n_new, int64_t n, int32_t *start,
+                                    int32_t *dev_status, void *stream);
+
+/*
+ * lcx_pages_fork -- sequence dst[i] becomes a copy of src[i]: full pages are
+ * shared (their counts grow), a partial last page is copied, in every layer,
+ * to a page from the free stack (the block rule of lcx_pages_extend).  All
+ * sources are read as they were before the call; one source may be forked
+ * several times.  Skipped: a negative src or dst; with a status: a number >=
+ * max_seqs, a dst that is not empty or seen earlier (LCX_ERR_INVALID_ARG),
+ * entries without a free page (LCX_ERR_NO_PAGES).
+ */
+LCX_API lcx_status lcx_pages_fork(const lcx_paged_cache *cache, const int32_t *src,
+                                  const int32_t *dst, int64_t n, int32_t *dev_status,
+                                  void *stream);
+
+/*
+ * lcx_pages_free -- the sequences end: their pages lose one holder each, pages
+ * without a holder return to the free stack in ascending order, the table rows
+ * become -1 and the lengths 0.  A negative seq_id is skipped; one >= max_seqs or
+ * seen earlier as well, with LCX_ERR_INVALID_ARG.
+ */
+LCX_API lcx_status lcx_pages_free(const lcx_paged_cache *cache, const int32_t *seq_ids,
+                                  int64_t n, int32_t *dev_status, void *stream);
+
+/*
+ * lcx_pages_compact -- move the used pages to the lowest numbers: with U used
+ * pages, the k-th used page >= U moves, in every layer, to the k-th free page
+ * < U.  Tables and counts follow; free_pages becomes num_pages - 1, .., U.
+ */
+LCX_API lcx_status lcx_pages_compact(const lcx_paged_cache *cache, int32_t *dev_status,
+                                     void *stream);
+
+/*
+ * lcx_pages_copy -- copy page src_pages[i] to dst_pages[i] in every layer; the
+ * bookkeeping is not touched.  Skipped with LCX_ERR_INVALID_ARG: a number
+ * outside [0, num_pages), a destination seen earlier or that is also a source
+ * of the call (a page copied to itself is left alone without a status); a
+ * negative source or destination is skipped silently.
+ */
+LCX_API lcx_status lcx_pages_copy(const lcx_paged_cache *cache, const int32_t *src_pages,
+                                  const int32_t *dst_pages, int64_t n, int32_t *dev_status,
+                                  void *stream);
+
+typedef struct {
+    const void *k, *v;         /* DEVICE [T, Hkv, D] new keys (un-rotated) and values  */
+    const void *q;             /* DEVICE [T, Hq, D] or NULL: queries to rotate along   */
+    void *q_out;               /* DEVICE [T, Hq, D] rotated queries (may be q), with q */
+    void *k_out;               /* DEVICE [T, Hkv, D] or NULL: rotated keys, packed
+                                  (may be k)                                          */
+    const int32_t *seq_ids;    /* DEVICE [n]                                          */
+    const int32_t *start;      /* DEVICE [n]: position of each entry's first token, as
+                                  lcx_pages_extend gives it; -1 skips the entry        */
+    const int32_t *cu_new;     /* DEVICE [n + 1] ascending: entry i's tokens are rows
+                                  cu_new[i] .. cu_new[i + 1] - 1; NULL: row i (T = n)  */
+    int32_t *dev_status;       /* DEVICE int32 or NULL                                */
+    int64_t n, T, Hq, layer;
+    int64_t k_strides[3], v_strides[3], q_strides[3], q_out_strides[3], k_out_strides[3];
+                               /* elements, per (token, head, dim)                     */
+    lcx_rope_params rope;      /* head_dim = D; seq_len > 0 for the length-dependent
+                                  modes (the lengths are device data)                 */
+} lcx_paged_append_args;
+
+/*
+ * lcx_paged_append -- rotate the new tokens' keys (times mscale, as
+ * lcx_apply_rope does, bit for bit) and write keys and values into their pages
+ * of one layer; optionally rotate the tokens' queries in the same pass.  Entry
+ * i's k-th token sits at position start[i] + k; a position at or beyond the
+ * sequence's length is not written (LCX_ERR_INVALID_ARG in the status word:
+ * extend first).  Rows of skipped entries and rows outside cu_new are neither
+ * read nor written.  Each position must be given once per call.
+ */
+LCX_API lcx_status lcx_paged_append(const lcx_paged_cache *cache,
+                                    const lcx_paged_append_args *args, void *stream);
+
+#define LCX_DECODE_PREROTATED 1u /* q is already rotated (mscale included) */
+
+typedef struct {
+    const void *q;             /* DEVICE [n, Hq, D], dtype of the cache                */
+    void *o;                   /* DEVICE [n, Hq, D]                                    */
+    float *lse;                /* DEVICE [n, Hq] contiguous, or NULL                   */
+    const int32_t *seq_ids;    /* DEVICE [n]; negative: a padded entry                 */
+    int32_t *dev_status;       /* DEVICE int32 or NULL                                 */
+    int64_t n, Hq, layer;
+    int64_t q_strides[3], o_strides[3];
+    lcx_rope_params rope;      /* head_dim = D, as for lcx_paged_append                */
+    int64_t window, sinks;     /* as lcx_attn_args; the query sits at seq_len - 1      */
+    float softmax_scale;       /* 0 -> 1/sqrt(D)                                       */
+    uint32_t flags;            /* LCX_DECODE_*                                         */
+} lcx_paged_decode_args;
+
+/* Workspace bytes lcx_paged_decode needs for n entries of Hq query heads
+ * (-1: sizes out of range). */
+LCX_API int64_t lcx_paged_decode_workspace_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64_t D);
+
+/*
+ * lcx_paged_decode -- attention of one new token per entry over its cached
+ * keys (the token's own among them: extend and append first):
+ *   o = sum_j softmax_j(c <q', k'_j>) v_j over j < seq_len, with a window W > 0
+ *   only seq_len - 1 - j < W or j < sinks; q' is q rotated at seq_len - 1.
+ * The keys of all entries are cut into equal shares of consecutive blocks, one
+ * share per CTA, and the parts of a query head joined by their softmax
+ * statistics (the merge of lcx_attn_merge) in a fixed order, so results do not
+ * vary from call to call.  An entry without keys (length 0, padded) gets o = 0 and
+ * lse = -inf.  Keys that the window hides, and slots behind the length, are
+ * never read.  seq_ids may name one sequence several times.
+ *   Supported: D 64 or 128, any Hq / Hkv; strides multiples of 16 bytes.
+ *   Arithmetic: 16-bit pools: bf16 tensor-core products with fp32
+ *   accumulation; with at most 8 query heads per kv head q' and the weights
+ *   enter as two bf16 parts each (16 bits of mantissa), else rounded to bf16.
+ *   fp32 pools: every operand as two tf32 parts (about 21 bits).
+ *   workspace : DEVICE, 256-byte aligned, lcx_paged_decode_workspace_bytes;
+ *               contents ignored and overwritten; not shared by calls in flight.
+ */
+LCX_API lcx_status lcx_paged_decode(const lcx_paged_cache *cache,
+                                    const lcx_paged_decode_args *args, void *workspace,
+                                    int64_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------ packed prompts */
+/* What a plan holds (written by lcx_varlen_plan, passed on by value). */
+typedef struct {
+    int64_t n_seqs, total_q, total_k, max_k; /* max_k: longest key length            */
+    int64_t n_units[2];        /* work units of 128 and of 256 query rows             */
+    int64_t ints;              /* int32 values of the plan                            */
+} lcx_varlen_info;
+
+/* int32 values of a plan for n sequences (-1: a negative length, or sums of
+ * 2^30 tokens and more).  Host only. */
+LCX_API int64_t lcx_varlen_plan_ints(const int32_t *lens_q, const int32_t *lens_k, int64_t n);
+
+/*
+ * lcx_varlen_plan -- lay out the work of packed sequences: lens_q[s] query rows
+ * and lens_k[s] key rows each (HOST arrays), packed one behind the other.
+ * Writes the plan (HOST, `ints` values; the caller copies it to the device) and
+ * info.  One plan serves every layer and head count.  Host only.
+ */
+LCX_API lcx_status lcx_varlen_plan(const int32_t *lens_q, const int32_t *lens_k, int64_t n,
+                                   int32_t *plan, int64_t ints, lcx_varlen_info *info);
+
+#define LCX_VARLEN_PREROTATED 1u /* q and k are already rotated (mscale included)      */
+
+typedef struct {
+    const void *q;             /* DEVICE [Tq, Hq, D], Tq >= total_q                    */
+    const void *k, *v;         /* DEVICE [Tk, Hkv, D], Tk >= total_k                   */
+    void *o;                   /* DEVICE [Tq, Hq, D]                                   */
+    float *lse;                /* DEVICE [Hq, Tq] contiguous, or NULL                  */
+    const int32_t *plan;       /* DEVICE copy of the plan, 16-byte aligned             */
+    void *k_rot;               /* DEVICE scratch [total_k, Hkv, D] of dtype for the
+                                  rotated keys; unused with LCX_VARLEN_PREROTATED or
+                                  rope mode NONE                                      */
+    int64_t k_rot_bytes;
+    int32_t *dev_status;       /* as lcx_attn_args                                     */
+    lcx_varlen_info info;      /* the plan's info                                      */
+    int32_t dtype, causal;
+    int64_t Tq, Tk, Hq, Hkv, D;
+    int64_t q_strides[3], k_strides[3], v_strides[3], o_strides[3]; /* (token, head, dim) */
+    lcx_rope_params rope;      /* head_dim = D; the length-dependent modes use the
+                                  plan's longest key length unless seq_len is set     */
+    int64_t window, sinks;     /* as lcx_attn_args                                     */
+    float softmax_scale;       /* 0 -> 1/sqrt(D)                                       */
+    uint32_t flags;            /* LCX_VARLEN_*                                         */
+    int32_t watchdog_ms, reserved0;
+} lcx_varlen_args;
+
+/*
+ * lcx_attn_varlen -- lcx_attn_fwd over packed sequences of different lengths:
+ * sequence s attends to its own keys only.  Its query i sits at position
+ * lens_k - lens_q + i, its key j at j (prompts: lens_q = lens_k; a later chunk
+ * of a prompt passes all keys so far).  Visibility, scale and rotation as for
+ * lcx_attn_fwd.  A query without a visible key (no keys, or more queries than
+ * keys) gets o = 0, lse = -inf.  Rows of o and lse at total_q and beyond are
+ * left as they were.  NaN or infinity in a key or value that a query does not
+ * see leaves that query alone.
+ *   Supported: D 64 or 128, full rotary; bf16 (tensor cores; q', k' and the
+ *   weights rounded to bf16, fp32 accumulation) or fp32 (fp32 arithmetic).
+ */
+LCX_API lcx_status lcx_attn_varlen(const lcx_varlen_args *args, void *stream);
 
 /* Static description of a status code. */
 LCX_API const char *lcx_status_string(lcx_status status);

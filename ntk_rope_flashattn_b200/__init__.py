@@ -33,7 +33,11 @@ LCX_ATTN_TEST_STALL = 0x80000000
 EXPORTED = ("lcx_rope_table", "lcx_apply_rope", "lcx_attn_fwd", "lcx_attn_fwd_split",
             "lcx_attn_split_workspace_bytes", "lcx_attn_merge", "lcx_attn_fwd_split_static",
             "lcx_status_string",
-            "lcx_last_error", "lcx_version")
+            "lcx_last_error", "lcx_version",
+            "lcx_paged_scratch_ints", "lcx_pages_extend", "lcx_pages_fork", "lcx_pages_free",
+            "lcx_pages_compact", "lcx_pages_copy", "lcx_paged_append", "lcx_paged_decode",
+            "lcx_paged_decode_workspace_bytes", "lcx_varlen_plan_ints", "lcx_varlen_plan",
+            "lcx_attn_varlen")
 
 
 class LcxError(RuntimeError):
@@ -43,7 +47,7 @@ class LcxError(RuntimeError):
 
 
 STATUS_NAMES = {0: "LCX_OK", 1: "LCX_ERR_INVALID_ARG", 2: "LCX_ERR_UNSUPPORTED",
-                3: "LCX_ERR_CUDA", 4: "LCX_ERR_TIMEOUT"}
+                3: "LCX_ERR_CUDA", 4: "LCX_ERR_TIMEOUT", 5: "LCX_ERR_NO_PAGES"}
 
 
 class _RopeParams(ctypes.Structure):
@@ -161,6 +165,8 @@ def load(path: str = LIB_PATH):
     lib.lcx_last_error.restype = ctypes.c_char_p
     lib.lcx_version.argtypes = []
     lib.lcx_version.restype = ctypes.c_int32
+    paged._declare(lib)
+    varlen._declare(lib)
     _lib = lib
     return lib
 
@@ -539,3 +545,10 @@ def attn_fwd_host(q, k, v, rope: RopeParams, device="cuda", workspace=None, chun
             copy_rows(o_host, o_dev, b, g0 * G, g1 * G, i0, i1)
     cur.wait_stream(s_out)
     return o_host
+
+
+from . import paged, varlen                                              # noqa: E402
+from .paged import (LCX_ERR_NO_PAGES, LCX_PAGES_MAX_ENTRIES, PagedCache,  # noqa: E402,F401
+                    paged_append, paged_decode, paged_decode_workspace_bytes, pages_compact,
+                    pages_copy, pages_extend, pages_fork, pages_free)
+from .varlen import VarlenPlan, attn_varlen                              # noqa: E402,F401

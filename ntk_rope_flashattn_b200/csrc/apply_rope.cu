@@ -17,6 +17,7 @@
 
 #include "lcx_internal.h"
 #include "rope_angle.cuh"
+#include "vec16.cuh"
 
 namespace lcx {
 namespace {
@@ -38,44 +39,6 @@ struct RopeArgs {
     float ms;
     float theta[kMaxHalf];
 };
-
-template <typename T>
-struct Vec;  // 16 bytes of T as 32-bit words
-template <>
-struct Vec<__nv_bfloat16> {
-    static constexpr int N = 8;  // elements per 16 bytes
-};
-template <>
-struct Vec<float> {
-    static constexpr int N = 4;
-};
-
-__device__ __forceinline__ void unpack(const uint4 &v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        x[2 * k] = __uint_as_float(w[k] << 16);
-        x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-    }
-}
-__device__ __forceinline__ void unpack(const uint4 &v, float (&x)[4]) {
-    x[0] = __uint_as_float(v.x);
-    x[1] = __uint_as_float(v.y);
-    x[2] = __uint_as_float(v.z);
-    x[3] = __uint_as_float(v.w);
-}
-__device__ __forceinline__ uint32_t pk(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint4 pack(const float (&y)[8]) {
-    return make_uint4(pk(y[0], y[1]), pk(y[2], y[3]), pk(y[4], y[5]), pk(y[6], y[7]));
-}
-__device__ __forceinline__ uint4 pack(const float (&y)[4]) {
-    return make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
-                      __float_as_uint(y[3]));
-}
 
 __device__ __forceinline__ uint32_t pk16(float lo, float hi) {
     uint32_t r;

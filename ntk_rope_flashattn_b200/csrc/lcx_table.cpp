@@ -152,6 +152,7 @@ const char *lcx_status_string(lcx_status status) {
         case LCX_ERR_UNSUPPORTED: return "unsupported argument combination";
         case LCX_ERR_CUDA: return "CUDA error";
         case LCX_ERR_TIMEOUT: return "device wait timed out";
+        case LCX_ERR_NO_PAGES: return "no free page in the cache";
     }
     return "unknown status";
 }

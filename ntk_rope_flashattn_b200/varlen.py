@@ -1,0 +1,157 @@
+"""Attention over packed prompts of different lengths: ``VarlenPlan`` and
+``attn_varlen`` (see ``lcx_attn_varlen`` in ``include/lcx.h``).
+
+    plan = lcx.VarlenPlan([512, 17, 2048])                # host lengths, once per batch
+    o = lcx.attn_varlen(q, k, v, plan, rope)              # q [T, Hq, D], k/v [T, Hkv, D]
+"""
+import ctypes
+
+import numpy as np
+
+from . import RopeParams, _check, _dtype_code, _RopeParams, _same_device, _stream, load
+
+LCX_VARLEN_PREROTATED = 1
+
+_P, _I64, _I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+
+
+class _Info(ctypes.Structure):
+    _fields_ = [("n_seqs", _I64), ("total_q", _I64), ("total_k", _I64), ("max_k", _I64),
+                ("n_units", _I64 * 2), ("ints", _I64)]
+
+
+class _VarlenArgs(ctypes.Structure):
+    _fields_ = [("q", _P), ("k", _P), ("v", _P), ("o", _P), ("lse", _P), ("plan", _P),
+                ("k_rot", _P), ("k_rot_bytes", _I64), ("dev_status", _P), ("info", _Info),
+                ("dtype", _I32), ("causal", _I32), ("Tq", _I64), ("Tk", _I64), ("Hq", _I64),
+                ("Hkv", _I64), ("D", _I64), ("q_strides", _I64 * 3), ("k_strides", _I64 * 3),
+                ("v_strides", _I64 * 3), ("o_strides", _I64 * 3), ("rope", _RopeParams),
+                ("window", _I64), ("sinks", _I64), ("softmax_scale", ctypes.c_float),
+                ("flags", ctypes.c_uint32), ("watchdog_ms", _I32), ("reserved0", _I32)]
+
+
+def _declare(lib):
+    lib.lcx_varlen_plan_ints.argtypes = [_P, _P, _I64]
+    lib.lcx_varlen_plan_ints.restype = _I64
+    lib.lcx_varlen_plan.argtypes = [_P, _P, _I64, _P, _I64, ctypes.POINTER(_Info)]
+    lib.lcx_varlen_plan.restype = ctypes.c_int
+    lib.lcx_attn_varlen.argtypes = [ctypes.POINTER(_VarlenArgs), _P]
+    lib.lcx_attn_varlen.restype = ctypes.c_int
+
+
+class VarlenPlan:
+    """The work layout of packed sequences (``lcx_varlen_plan``): ``seqlens_q[s]``
+    query rows and ``seqlens_k[s]`` key rows each (the same when not given), host
+    integers.  One plan serves every layer of a batch; it does not change."""
+
+    def __init__(self, seqlens_q, seqlens_k=None, device="cuda"):
+        import torch
+        device = torch.device(device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        lens = []
+        for x in (seqlens_q, seqlens_q if seqlens_k is None else seqlens_k):
+            if isinstance(x, torch.Tensor) and x.is_cuda:
+                raise ValueError("sequence lengths are host integers (got a CUDA tensor)")
+            a = np.asarray(x, dtype=np.int64).reshape(-1)
+            if a.size and (a.min() < 0 or a.max() > 2 ** 30):
+                raise ValueError("sequence lengths must be in [0, 2^30]")
+            lens.append(np.ascontiguousarray(a, np.int32))
+        if lens[0].size != lens[1].size:
+            raise ValueError("seqlens_q and seqlens_k must have the same length")
+        n, pq, pk = lens[0].size, lens[0].ctypes.data, lens[1].ctypes.data
+        ints = int(load().lcx_varlen_plan_ints(pq, pk, n))
+        if ints < 0:
+            raise ValueError("sequence lengths sum to more than 2^30")
+        host = torch.zeros(ints, dtype=torch.int32)
+        self.info = _Info()
+        _check(load().lcx_varlen_plan(pq, pk, n, host.data_ptr(), ints, ctypes.byref(self.info)))
+        self.device = device
+        self.plan = host.to(device)
+
+    @property
+    def total_q(self) -> int:
+        return int(self.info.total_q)
+
+    @property
+    def total_k(self) -> int:
+        return int(self.info.total_k)
+
+    @property
+    def cu_q(self):
+        """int32 [n + 1] device tensor: first packed query row of each sequence."""
+        n = int(self.info.n_seqs)
+        return self.plan[8:8 + n + 1]
+
+    @property
+    def cu_k(self):
+        """int32 [n + 1] device tensor: first packed key row of each sequence."""
+        n = int(self.info.n_seqs)
+        return self.plan[9 + n:9 + n + n + 1]
+
+
+def _strides3(t):
+    return (_I64 * 3)(*[int(s) for s in t.stride()])
+
+
+def attn_varlen(q, k, v, plan: VarlenPlan, rope: RopeParams, causal: bool = True, window: int = 0,
+                sinks: int = 0, softmax_scale: float = 0.0, return_lse: bool = False,
+                prerotated: bool = False, out=None, lse=None, k_rot=None, status=None,
+                watchdog_ms: int = 0):
+    """Fused RoPE + causal attention over the plan's packed sequences.
+
+    q [Tq, Hq, D], k/v [Tk, Hkv, D] CUDA tensors (bf16 or fp32, last dim
+    contiguous) holding the sequences one behind the other; query i of a sequence
+    sits at position len_k - len_q + i, key j at j.  Returns o [Tq, Hq, D] (and
+    lse [Hq, Tq] fp32 if asked); rows behind the last sequence are left as they
+    were (zero when the call allocates o and lse itself).  ``prerotated``: q and k
+    are already rotated
+    (``paged_append``'s q_out and k_out); otherwise the keys are rotated once into
+    ``k_rot`` (allocated when not given).  A query without a visible key gets
+    o = 0 and lse = -inf.  ``status`` and ``watchdog_ms`` as for ``attn_fwd``."""
+    import torch
+    for t in (q, k, v):
+        if t.dim() != 3 or not t.is_cuda:
+            raise ValueError("q, k, v must be 3-D CUDA tensors [tokens, heads, D]")
+    Tq, Hq, D = q.shape
+    Tk, Hkv = k.shape[0], k.shape[1]
+    if k.shape != (Tk, Hkv, D) or v.shape != k.shape:
+        raise ValueError("shape mismatch: q %s k %s v %s" % (q.shape, k.shape, v.shape))
+    if not (q.dtype == k.dtype == v.dtype):
+        raise ValueError("q, k, v must share a dtype")
+    _same_device(q, k=k, v=v, out=out, lse=lse, k_rot=k_rot, status=status, plan=plan.plan)
+    whole = plan.total_q == Tq
+    alloc = torch.empty if whole else torch.zeros
+    o = out if out is not None else alloc((Tq, Hq, D), dtype=q.dtype, device=q.device)
+    if o.shape != q.shape or o.dtype != q.dtype:
+        raise ValueError("out must be shaped like q")
+    if return_lse and lse is None:
+        lse = alloc((Hq, Tq), dtype=torch.float32, device=q.device)
+    if lse is not None and (lse.shape != (Hq, Tq) or lse.dtype != torch.float32 or
+                            not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous fp32 [%d, %d]" % (Hq, Tq))
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise ValueError("status must be an int32 tensor")
+    a = _VarlenArgs()
+    a.q, a.k, a.v, a.o = q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr()
+    a.lse = None if lse is None else lse.data_ptr()
+    a.plan, a.info = plan.plan.data_ptr(), plan.info
+    a.dev_status = None if status is None else status.data_ptr()
+    if not prerotated and rope.mode != "none" and k_rot is None:
+        k_rot = torch.empty((max(plan.total_k, 1), Hkv, D), dtype=k.dtype, device=k.device)
+    if k_rot is not None:
+        if not k_rot.is_contiguous():
+            raise ValueError("k_rot must be contiguous")
+        a.k_rot, a.k_rot_bytes = k_rot.data_ptr(), k_rot.numel() * k_rot.element_size()
+    a.dtype, a.causal = _dtype_code(q), 1 if causal else 0
+    a.Tq, a.Tk, a.Hq, a.Hkv, a.D = Tq, Tk, Hq, Hkv, D
+    a.q_strides, a.k_strides = _strides3(q), _strides3(k)
+    a.v_strides, a.o_strides = _strides3(v), _strides3(o)
+    rope_c = rope._c()
+    a.rope = rope_c
+    a.window, a.sinks, a.softmax_scale = int(window), int(sinks), float(softmax_scale)
+    a.flags = LCX_VARLEN_PREROTATED if prerotated else 0
+    a.watchdog_ms = int(watchdog_ms)
+    with torch.cuda.device(q.device):
+        _check(load().lcx_attn_varlen(ctypes.byref(a), _stream(q)))
+    return (o, lse) if return_lse else o

@@ -1,0 +1,408 @@
+"""paged_append and paged_decode on the GPU against their plain 64-bit forms
+(bounds: serving_plain)."""
+import dataclasses
+import random
+
+import pytest
+import torch
+
+import ntk_rope_flashattn_b200 as lcx
+from serving_plain import attend, check, rotate
+
+pytestmark = pytest.mark.gpu
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def word():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def randn(seed, *shape, dtype=torch.bfloat16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda").to(dtype)
+
+
+def cache_of(lens, ps=16, H=2, D=128, dtype=torch.bfloat16, layers=1, extra=3, seed=0, nhd=False,
+             fill=float("nan")):
+    """A cache whose pools hold NaN wherever no token is, sequences of these lengths
+    in shuffled pages filled with N(0, 1) keys and values."""
+    mp = max(max(-(-x // ps) for x in lens), 1) + 1
+    P = sum(-(-x // ps) for x in lens) + extra
+    shape = (layers, P, ps, H, D)
+    kw = {}
+    for f in ("k_pages", "v_pages"):
+        t = torch.full(shape if nhd else (layers, P, H, ps, D), fill, dtype=dtype, device="cuda")
+        kw[f] = t if nhd else t.transpose(2, 3)
+    c = lcx.PagedCache(P, ps, H, D, len(lens), mp, num_layers=layers, dtype=dtype, **kw)
+    order = list(range(P))
+    random.Random(seed).shuffle(order)
+    c.free_pages.copy_(ints(order))
+    lcx.pages_extend(c, ints(list(range(len(lens)))), ints(lens))
+    rows = []
+    for s, n in enumerate(lens):
+        k, v = randn(seed + 2 * s, n, H, D, dtype=dtype), randn(seed + 2 * s + 1, n, H, D, dtype=dtype)
+        pos = torch.arange(n, device="cuda")
+        pg, sl = c.block_table[s].long()[pos // ps], pos % ps
+        for x in range(layers):
+            c.k_pages[x, pg, sl] = k
+            c.v_pages[x, pg, sl] = v
+        rows.append((k.double().cpu(), v.double().cpu()))
+    return c, rows
+
+
+def plain_decode(q, rows, lens, ids, rope, window=0, sinks=0, scale=None, prerotated=False):
+    q = q.double().cpu()
+    scale = q.shape[-1] ** -0.5 if scale is None else scale
+    parts = []
+    for e, s in enumerate(ids):
+        n = lens[s] if s >= 0 else 0
+        k, v = (x[:n] for x in rows[s]) if s >= 0 else (torch.zeros(0, 1, q.shape[-1]).double(),) * 2
+        if s < 0:
+            k = v = torch.zeros(0, rows[0][0].shape[1], q.shape[-1]).double()
+        pos = torch.tensor([n - 1])
+        qe = q[e:e + 1] if prerotated else rotate(q[e:e + 1], pos, rope)
+        parts.append(attend(qe, k, v, pos, True, window, sinks, scale))
+    return (torch.cat([p[0] for p in parts]), torch.cat([p[1] for p in parts], 1).T,
+            torch.cat([p[2] for p in parts]), torch.cat([p[3] for p in parts], 1).T)
+
+
+def arithmetic(dtype, G, n):
+    """(u_s, u_p) of paged_decode for G query heads per kv head and n keys.  fp32
+    sums of D = 128 products and of n weights; operands in two parts of bf16 (or
+    of tf32), or (16-bit pools, G > 8) one bf16 part."""
+    acc, accp = 128 * 2.0 ** -24, n * 2.0 ** -24 + 2.0 ** -20
+    if dtype == torch.float32:
+        return 3 * 2.0 ** -22 + acc, 3 * 2.0 ** -22 + accp
+    if G <= 8:
+        return 2.0 ** -16 + acc, 2.0 ** -16 + accp
+    return 2.0 ** -8 + acc, 2.0 ** -8 + accp
+
+
+def check_decode(o, lse, want, dtype, G, n, label=""):
+    wo, wl, wm, wp = want
+    u_s, u_p = arithmetic(dtype, G, n)
+    check(o, lse.T, (wo, wl.T, wm, wp.T), u_s, u_p, label)
+
+
+CASES = [
+    # lens, ps, Hq, H, D, dtype, window, sinks, kind
+    ([1], 16, 2, 2, 64, "bf16", 0, 0, {}),
+    ([17, 1, 0, 300, 16], 16, 8, 2, 128, "bf16", 0, 0, {}),
+    ([1000, 63, 64, 65, 129], 8, 8, 1, 64, "bf16", 0, 0, {}),
+    ([700, 2], 1, 5, 1, 128, "bf16", 0, 0, {}),
+    ([2500, 31], 128, 12, 1, 128, "bf16", 0, 0, {}),            # 12 heads a group
+    ([900, 40, 333], 32, 48, 2, 64, "bf16", 0, 0, {}),          # 24 heads a group
+    ([5000, 77], 64, 6, 2, 128, "bf16", 100, 4, {}),
+    ([5000, 10, 200], 16, 4, 4, 64, "bf16", 1, 0, {}),
+    ([3000, 60], 16, 16, 2, 128, "bf16", 64, 130, dict(nhd=True)),
+    ([555, 1, 0, 64], 16, 8, 2, 128, "f32", 0, 0, {}),
+    ([1234, 9], 32, 5, 1, 64, "f32", 0, 0, dict(nhd=True)),
+    ([700, 33], 8, 24, 2, 128, "f32", 50, 3, {}),
+    ([4097], 1024, 32, 2, 64, "f32", 0, 0, {}),
+]
+
+
+@pytest.mark.parametrize("lens,ps,Hq,H,D,dt,window,sinks,kw", CASES)
+@pytest.mark.parametrize("mode", ["yarn"])
+def test_decode(lens, ps, Hq, H, D, dt, window, sinks, kw, mode):
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    rope = lcx.RopeParams(mode, D, scale=4.0, original_max_pos=1024, base=500000.0)
+    c, rows = cache_of(lens, ps, H, D, dtype, seed=len(lens) + ps, **kw)
+    ids = list(range(len(lens))) + [-1, 0]
+    q = randn(99, len(ids), Hq, D, dtype=dtype)
+    status = word()
+    o, lse = lcx.paged_decode(c, q, ints(ids), rope, window=window, sinks=sinks, return_lse=True,
+                              status=status)
+    want = plain_decode(q, rows, lens, ids, rope, window, sinks)
+    check_decode(o, lse, want, dtype, Hq // H, max(lens), "decode %s" % lens)
+    assert int(status) == 0
+    # deterministic: a second call gives the same bits
+    o2, lse2 = lcx.paged_decode(c, q, ints(ids), rope, window=window, sinks=sinks, return_lse=True)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("pairing", ["half", "interleaved"])
+@pytest.mark.parametrize("mode", ["none", "plain", "pi", "ntk", "dynamic_ntk"])
+def test_decode_modes_and_prerotated(mode, pairing):
+    rope = lcx.RopeParams(mode, 64, scale=2.0, original_max_pos=100, pairing=pairing, seq_len=400)
+    lens = [77, 400]
+    c, rows = cache_of(lens, 16, 2, 64, torch.float32)
+    q = randn(5, 2, 6, 64, dtype=torch.float32)
+    o, lse = lcx.paged_decode(c, q, ints([0, 1]), rope, return_lse=True)
+    check_decode(o, lse, plain_decode(q, rows, lens, [0, 1], rope), torch.float32, 3, 400, mode)
+    o, lse = lcx.paged_decode(c, q, ints([1, 0]), rope, return_lse=True, prerotated=True,
+                              softmax_scale=0.3)
+    check_decode(o, lse, plain_decode(q, rows, lens, [1, 0], rope, scale=0.3, prerotated=True),
+                 torch.float32, 3, 400, "prerotated")
+
+
+def test_decode_strided_tensors_and_layers():
+    lens = [150, 20]
+    rope = lcx.RopeParams("plain", 128)
+    c, rows = cache_of(lens, 16, 2, 128, layers=3)
+    c.k_pages[0], c.k_pages[2] = float("nan"), float("nan")   # only layer 1 is read
+    big = randn(3, 2, 3, 8, 128)
+    q = big[:, 1]
+    out = torch.full((2, 10, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lcx.paged_decode(c, q, ints([1, 0]), rope, layer=1, out=out[:, 1:9])
+    o, lse = lcx.paged_decode(c, q.contiguous(), ints([1, 0]), rope, layer=1, return_lse=True)
+    assert torch.equal(out[:, 1:9], o)
+    assert (out[:, 0] == 7).all() and (out[:, 9] == 7).all()
+    check_decode(o, lse, plain_decode(q, rows, lens, [1, 0], rope), torch.bfloat16, 4, 150)
+
+
+def test_decode_hidden_values_are_never_read():
+    """NaN and infinity in keys and values that the window hides, in free slots of
+    the last page and in other sequences' pages change nothing; in a visible key
+    they reach the output."""
+    lens = [500, 90]
+    rope = lcx.RopeParams("plain", 64)
+    for dtype in (torch.bfloat16, torch.float32):
+        c, rows = cache_of(lens, 16, 2, 64, dtype)
+        q = randn(8, 2, 8, 64, dtype=dtype)
+        a = lcx.paged_decode(c, q, ints([0, 1]), rope, window=37, sinks=3)
+        for j, bad in ((10, float("nan")), (3, float("inf")), (462, -float("inf")), (400, float("nan"))):
+            pg, sl = int(c.block_table[0, j // 16]), j % 16
+            c.k_pages[0, pg, sl] = bad
+            c.v_pages[0, pg, sl] = bad
+        b = lcx.paged_decode(c, q, ints([0, 1]), rope, window=37, sinks=3)
+        assert torch.equal(a, b) and torch.isfinite(a.float()).all()
+        pg, sl = int(c.block_table[0, 470 // 16]), 470 % 16
+        c.v_pages[0, pg, sl, 1, 5] = float("nan")
+        b = lcx.paged_decode(c, q, ints([0, 1]), rope, window=37, sinks=3)
+        assert torch.isnan(b[0, 4:, 5].float()).all()
+        assert torch.equal(a[1], b[1]) and torch.equal(a[0, :4], b[0, :4])
+        c.k_pages[0, pg, sl, 0, 3] = float("nan")
+        b = lcx.paged_decode(c, q, ints([0, 1]), rope, window=37, sinks=3)
+        assert torch.isnan(b[0, :4].float()).all()
+
+
+def test_decode_bad_numbers_are_hidden_and_reported():
+    lens = [70, 40, 50]
+    rope = lcx.RopeParams("plain", 64)
+    c, rows = cache_of(lens, 16, 2, 64)
+    q = randn(8, 4, 4, 64)
+    good = lcx.paged_decode(c, q, ints([0, 1, 2, 1]), rope)
+    status = word()
+    b = lcx.paged_decode(c, q, ints([0, 1, 3, 1]), rope, status=status)       # sequence 3 of 3
+    assert int(status) == lcx.LCX_ERR_INVALID_ARG
+    assert torch.equal(b[[0, 1, 3]], good[[0, 1, 3]]) and (b[2] == 0).all()
+    status.zero_()
+    c.block_table[0, 1] = c.num_pages                      # no such page: keys 16..31 hidden
+    b, lse = lcx.paged_decode(c, q, ints([0, 1, 2, 1]), rope, status=status, return_lse=True)
+    assert int(status) == lcx.LCX_ERR_INVALID_ARG and torch.equal(b[1:], good[1:])
+    k, v = rows[0]
+    keep = [j for j in range(70) if not 16 <= j < 32]
+    qe = rotate(q[:1].double().cpu(), torch.tensor([69]), rope)
+    want = attend(qe, k[keep], v[keep], torch.tensor([69]), True, 0, 0, 64 ** -0.5)
+    check(b[:1], lse[:1].T, want, *arithmetic(torch.bfloat16, 2, 70))
+    status.zero_()
+    c.seq_lens[1] = 10 ** 6                                # beyond the table: cut there
+    c.block_table[1] = -1
+    b, lse = lcx.paged_decode(c, q, ints([0, 1, 2, 1]), rope, status=status, return_lse=True)
+    assert int(status) == lcx.LCX_ERR_INVALID_ARG
+    assert (b[1] == 0).all() and torch.isinf(lse[1]).all() and torch.equal(b[2], good[2])
+
+
+def test_decode_on_another_stream_with_its_own_workspace():
+    lens = [3000, 100]
+    rope = lcx.RopeParams("plain", 128)
+    c, _ = cache_of(lens, 16, 2, 128)
+    q = randn(4, 2, 8, 128)
+    want = lcx.paged_decode(c, q, ints([0, 1]), rope)
+    ws = torch.empty(max(lcx.paged_decode_workspace_bytes(c, 2, 8), 256), dtype=torch.uint8,
+                     device="cuda").fill_(255)
+    ids = ints([0, 1])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = lcx.paged_decode(c, q, ids, rope, workspace=ws)
+    s.synchronize()
+    assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("pairing", ["half", "interleaved"])
+@pytest.mark.parametrize("D,H,Hq,ps,dt,nhd", [(64, 1, 3, 8, "bf16", False),
+                                              (128, 8, 32, 16, "bf16", True),
+                                              (64, 4, 4, 1, "f32", False),
+                                              (128, 2, 10, 64, "f32", True)])
+def test_append_equals_apply_rope(D, H, Hq, ps, dt, nhd, pairing):
+    """Keys land in their pages exactly as apply_rope rotates them, values as they
+    are, and nothing else is touched."""
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    rope = lcx.RopeParams("yarn", D, scale=8.0, original_max_pos=512, pairing=pairing)
+    old, new = [30, 0, 7, 511], [1, 40, 0, 130]
+    c, rows = cache_of(old, ps, H, D, dtype, layers=2, extra=400, nhd=nhd, fill=3.0)
+    ids = [3, 1, -1, 2, 0]
+    cnt = [new[3], new[1], 5, new[2], new[0]]
+    # the table of cache_of has no room for 511 + 130 tokens beyond one page: grow it
+    big = lcx.PagedCache(c.num_pages, ps, H, D, 4, 700, num_layers=2, dtype=dtype,
+                         k_pages=c.k_pages, v_pages=c.v_pages)
+    big.block_table.fill_(-1)
+    big.block_table[:, :c.max_pages_per_seq] = c.block_table
+    for f in ("seq_lens", "ref_counts", "free_pages", "n_free"):
+        getattr(big, f).copy_(getattr(c, f))
+    c = big
+    start = lcx.pages_extend(c, ints(ids), ints(cnt))
+    assert start.tolist() == [511, 0, -1, 7, 30]
+    cu = [0]
+    for x in cnt:
+        cu.append(cu[-1] + x)
+    T = cu[-1] + 2                                      # rows behind the last entry
+    k, v, q = (randn(i, T, h, D, dtype=dtype) for i, h in ((1, H), (2, H), (3, Hq)))
+    q_out, k_out = torch.full_like(q, 9.0), torch.full_like(k, 9.0)
+    kp, vp = c.k_pages.clone(), c.v_pages.clone()
+    lcx.paged_append(c, k, v, ints(ids), start, rope, layer=1, cu_new=ints(cu), q=q, q_out=q_out,
+                     k_out=k_out)
+    wq, wk = torch.full_like(q, 9.0), torch.full_like(k, 9.0)
+    for i, s in enumerate(ids):
+        if s < 0 or cnt[i] == 0:
+            continue
+        r = slice(cu[i], cu[i + 1])
+        p0 = int(start[i])
+        for x, w in ((q, wq), (k, wk)):
+            w[r] = lcx.apply_rope(x[r].transpose(0, 1)[None].contiguous(), rope,
+                                  pos_offset=p0)[0].transpose(0, 1)
+        pos = torch.arange(p0, p0 + cnt[i], device="cuda")
+        pg, sl = c.block_table[s].long()[pos // ps], pos % ps
+        kp[1, pg, sl], vp[1, pg, sl] = wk[r], v[r]
+    assert torch.equal(c.k_pages, kp) and torch.equal(c.v_pages, vp)
+    assert torch.equal(q_out, wq) and torch.equal(k_out, wk)
+    # in place, into the other layer
+    k2, q2 = k.clone(), q.clone()
+    lcx.paged_append(c, k2, v, ints(ids), start, rope, cu_new=ints(cu), q=q2, q_out=q2, k_out=k2)
+    wq[wq == 9.0], wk[wk == 9.0] = q[wq == 9.0], k[wk == 9.0]
+    assert torch.equal(q2, wq) and torch.equal(k2, wk)
+
+
+def test_append_far_positions():
+    """Angles stay exact near position 10^6 (the plain form in 64 bits)."""
+    rope = lcx.RopeParams("plain", 64)
+    c = lcx.PagedCache(4, 1024, 1, 64, 1, 2 ** 20, dtype=torch.float32)
+    n = 10 ** 6
+    c.seq_lens[0] = n + 3
+    c.block_table[0, n // 1024] = 2
+    k = randn(1, 3, 1, 64, dtype=torch.float32)
+    lcx.paged_append(c, k, k, ints([0]), ints([n]), rope, cu_new=ints([0, 3]))
+    want = rotate(k.cpu(), torch.arange(n, n + 3), rope)
+    got = c.k_pages[0, 2, n % 1024:n % 1024 + 3].double().cpu()
+    # one rounding of the angle (|phi| <= pi: 2^-23), of cos/sin and two products
+    assert (got - want).abs().max() <= 8 * 2.0 ** -22 * float(k.abs().max())
+
+
+def test_append_refuses_unreserved_positions():
+    c, _ = cache_of([5, 5], 4, 1, 64, fill=1.0)
+    rope = lcx.RopeParams("plain", 64)
+    status = word()
+    kp, vp = c.k_pages.clone(), c.v_pages.clone()
+    k = randn(0, 4, 1, 64)
+    # beyond the length, no such sequence, a negative start, a bad page
+    lcx.paged_append(c, k, k, ints([0, 2, 1, -1]), ints([5, 0, -1, 0]), rope, status=status)
+    assert torch.equal(c.k_pages, kp) and torch.equal(c.v_pages, vp)
+    assert int(status) == lcx.LCX_ERR_INVALID_ARG
+    c.block_table[1, 1] = c.num_pages + 7
+    status.zero_()
+    lcx.paged_append(c, k[:1], k[:1], ints([1]), ints([4]), rope, status=status)
+    assert torch.equal(c.k_pages, kp) and int(status) == lcx.LCX_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------ together
+def test_a_run_of_them_together():
+    """Prompts through packed prefill and append, decode steps, a fork, an end and a
+    compaction: decode agrees with attn_fwd over the same tokens."""
+    D, H, Hq, ps = 128, 2, 8, 16
+    rope = lcx.RopeParams("yarn", D, scale=4.0, original_max_pos=256)
+    lens = [40, 129, 7]
+    c = lcx.PagedCache(64, ps, H, D, 6, 20)
+    plan = lcx.VarlenPlan(lens)
+    T = sum(lens)
+    q, k, v = (randn(i, T, h, D) for i, h in ((1, Hq), (2, H), (3, H)))
+    ids = ints([0, 1, 2])
+    start = lcx.pages_extend(c, ids, ints(lens))
+    k_out = torch.empty_like(k)
+    q_out = lcx.paged_append(c, k, v, ids, start, rope, cu_new=plan.cu_q, q=q, k_out=k_out)
+    o = lcx.attn_varlen(q, k, v, plan, rope)
+    o2 = lcx.attn_varlen(q_out, k_out, v, plan, rope, prerotated=True)
+    hist = []
+    a = 0
+    for s, n in enumerate(lens):
+        r = slice(a, a + n)
+        a += n
+        x = [t[r].transpose(0, 1)[None] for t in (q, k, v)]
+        w = lcx.attn_fwd(*x, rope)[0].transpose(0, 1)
+        for got in (o[r], o2[r]):       # two bf16 paths: each within 2e-2 of exact
+            assert (got.float() - w.float()).abs().max() <= 4e-2
+        hist.append([x[1], x[2]])
+
+    def step(entries, seed, swap=False):
+        n = len(entries)
+        qs, ks, vs = (randn(seed + i, n, h, D) for i, h in ((1, Hq), (2, H), (3, H)))
+        e = ints(entries)
+        st = lcx.pages_extend(c, e)
+        lcx.paged_append(c, ks, vs, e, st, rope)
+        got = lcx.paged_decode(c, qs, e, rope)
+        for i, s in enumerate(entries):
+            hist[s] = [torch.cat([hist[s][0], ks[i][None, :, None]], 2),
+                       torch.cat([hist[s][1], vs[i][None, :, None]], 2)]
+            L = hist[s][0].shape[2]
+            w = lcx.attn_fwd(qs[i][None, :, None], hist[s][0], hist[s][1], rope, q_offset=L - 1)
+            assert (got[i].float() - w[0, :, 0].float()).abs().max() <= 4e-2
+        return qs, e, got
+
+    for i in range(12):
+        step([0, 1, 2], 100 + 10 * i)
+    lcx.pages_fork(c, ints([1, 1]), ints([4, 5]))
+    hist += [None, list(hist[1]), list(hist[1])]
+    step([4, 0, 5, 1], 400)
+    lcx.pages_free(c, ints([1, 2]))
+    qs, e, got = step([5, 0, 4], 500)
+    lcx.pages_compact(c)
+    assert torch.equal(lcx.paged_decode(c, qs, e, rope), got)
+    used = int((c.ref_counts > 0).sum())
+    assert (c.ref_counts[:used] > 0).all() and int(c.n_free) == c.num_pages - used
+    step([4, 5, 0], 600)
+
+
+def test_decode_step_replays_from_a_graph():
+    """extend + append + decode captured once; two graphs with workspaces of their
+    own, replayed in turn, equal eager steps on a twin cache."""
+    D, H, Hq = 64, 2, 4
+    rope = lcx.RopeParams("plain", D)
+    lens = [100, 3, 0]
+    (a, _), (b, _) = cache_of(lens, 16, H, D, extra=30), cache_of(lens, 16, H, D, extra=30)
+    ids = ints([0, 1, 2])
+    q, k, v = (randn(i, 3, h, D) for i, h in ((1, Hq), (2, H), (3, H)))
+    need = max(lcx.paged_decode_workspace_bytes(a, 3, Hq), 256)
+
+    def step(c, ws):
+        st = lcx.pages_extend(c, ids)
+        lcx.paged_append(c, k, v, ids, st, rope)
+        return lcx.paged_decode(c, q, ids, rope, workspace=ws)
+
+    meta = a.meta.clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(a, None)
+    torch.cuda.current_stream().wait_stream(s)
+    a.meta.copy_(meta)
+    graphs = []
+    for _ in range(2):
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o = step(a, ws)
+        graphs.append((g, o, ws))
+    a.meta.copy_(meta)
+    for i in range(6):
+        for t in (q, k, v):
+            t.copy_(randn(i + t.shape[1], *t.shape))
+        g, o, _ = graphs[i % 2]
+        g.replay()
+        want = step(b, None)
+        assert torch.equal(o, want)
+        assert torch.equal(a.seq_lens, b.seq_lens)

@@ -1,0 +1,213 @@
+"""attn_varlen on the GPU against the plain 64-bit form (bounds: serving_plain)
+and, for bf16, the library's own tolerance (max-abs 2e-2, mean-abs 2e-3)."""
+import pytest
+import torch
+
+import ntk_rope_flashattn_b200 as lcx
+from serving_plain import attend, check, rotate
+
+pytestmark = pytest.mark.gpu
+
+
+def randn(seed, *shape, dtype=torch.bfloat16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda").to(dtype)
+
+
+def plain(q, k, v, lq, lk, rope, causal=True, window=0, sinks=0, scale=None, prerotated=False):
+    q, k, v = (x.double().cpu() for x in (q, k, v))
+    scale = q.shape[-1] ** -0.5 if scale is None else scale
+    parts, a, b = [], 0, 0
+    for nq, nk in zip(lq, lk):
+        qp = torch.arange(nq) + (nk - nq)
+        qs, ks = q[a:a + nq], k[b:b + nk]
+        if not prerotated:
+            qs, ks = rotate(qs, qp, rope), rotate(ks, torch.arange(nk), rope)
+        parts.append(attend(qs, ks, v[b:b + nk], qp, causal, window, sinks, scale))
+        a, b = a + nq, b + nk
+    return (torch.cat([p[0] for p in parts]), torch.cat([p[1] for p in parts], 1),
+            torch.cat([p[2] for p in parts]), torch.cat([p[3] for p in parts], 1))
+
+
+def arithmetic(dtype, n):
+    """(u_s, u_p): bf16 rounds q', k' and the weights (the sums run over the unrounded
+    weights); fp32 rounds nothing but its sums (and q', k' to fp32)."""
+    acc = 128 * 2.0 ** -24 + 2.0 ** -21
+    if dtype == torch.bfloat16:
+        return 2.0 ** -7 + 2.0 ** -16 + acc, 2.0 ** -8 + n * 2.0 ** -24 + 2.0 ** -20
+    return 2.0 ** -22 + acc, n * 2.0 ** -24 + 2.0 ** -20
+
+
+def compare(o, lse, want, dtype, n, label=""):
+    check(o, lse, want, *arithmetic(dtype, n), label)
+    if dtype == torch.bfloat16:
+        err = (o.double().cpu() - want[0]).abs()
+        half = torch.where(want[0].abs() >= 4, torch.exp2(torch.floor(torch.log2(
+            want[0].abs().clamp(min=1e-30))) - 8), torch.zeros(()).double())
+        assert float((err - half).max()) <= 2e-2 and float(err.mean()) <= 2e-3
+
+
+LENS = [
+    ([1], None), ([5, 1, 0, 3], None), ([128, 127, 129], None), ([64, 300, 1, 0, 257], None),
+    ([1, 2, 130], [400, 131, 130]), ([10, 200, 0], [3, 200, 9]), ([600], [1000]),
+]
+
+
+@pytest.mark.parametrize("lq,lk", LENS)
+@pytest.mark.parametrize("Hq,H,D,dt", [(2, 2, 64, "bf16"), (8, 2, 128, "bf16"),
+                                       (3, 1, 128, "bf16"), (10, 2, 64, "bf16"),
+                                       (4, 2, 64, "f32"), (3, 1, 128, "f32")])
+def test_packed_lengths(lq, lk, Hq, H, D, dt):
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    lk = lq if lk is None else lk
+    rope = lcx.RopeParams("yarn", D, scale=4.0, original_max_pos=64)
+    q, k, v = (randn(i, n, h, D, dtype=dtype)
+               for i, n, h in ((1, sum(lq), Hq), (2, sum(lk), H), (3, sum(lk), H)))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, lse = lcx.attn_varlen(q, k, v, lcx.VarlenPlan(lq, lk), rope, return_lse=True, status=status)
+    assert int(status) == 0
+    compare(o, lse, plain(q, k, v, lq, lk, rope), dtype, max(lk), "%s" % lq)
+    o2, lse2 = lcx.attn_varlen(q, k, v, lcx.VarlenPlan(lq, lk), rope, return_lse=True)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (7, 0), (130, 3), (200, 150), (1000, 4)])
+@pytest.mark.parametrize("Hq,H,D,dt", [(4, 2, 64, "bf16"), (3, 1, 128, "bf16"), (2, 1, 64, "f32")])
+def test_window_and_sinks(window, sinks, Hq, H, D, dt):
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    lq, lk = [513, 40, 90], [513, 40, 700]
+    rope = lcx.RopeParams("plain", D)
+    q, k, v = (randn(i, n, h, D, dtype=dtype)
+               for i, n, h in ((1, sum(lq), Hq), (2, sum(lk), H), (3, sum(lk), H)))
+    o, lse = lcx.attn_varlen(q, k, v, lcx.VarlenPlan(lq, lk), rope, window=window, sinks=sinks,
+                             return_lse=True)
+    compare(o, lse, plain(q, k, v, lq, lk, rope, True, window, sinks), dtype, 700)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("mode,pairing", [("none", "half"), ("plain", "interleaved"),
+                                          ("ntk", "half"), ("dynamic_ntk", "half"),
+                                          ("pi", "interleaved")])
+def test_modes_not_causal_prerotated(mode, pairing, dt):
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    lq, lk = [100, 3, 140], [100, 250, 20]
+    # dynamic NTK takes the plan's longest key length
+    import dataclasses
+    rope = lcx.RopeParams(mode, 128, scale=2.0, original_max_pos=50, pairing=pairing)
+    fixed = dataclasses.replace(rope, seq_len=250)
+    q, k, v = (randn(i, n, h, 128, dtype=dtype) for i, n, h in ((1, 243, 4), (2, 370, 2), (3, 370, 2)))
+    plan = lcx.VarlenPlan(lq, lk)
+    o, lse = lcx.attn_varlen(q, k, v, plan, rope, causal=False, return_lse=True, softmax_scale=0.05)
+    compare(o, lse, plain(q, k, v, lq, lk, fixed, causal=False, scale=0.05), dtype, 250, mode)
+    o, lse = lcx.attn_varlen(q, k, v, plan, rope, prerotated=True, return_lse=True)
+    compare(o, lse, plain(q, k, v, lq, lk, fixed, prerotated=True), dtype, 250, "prerotated")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_strides_and_rows_behind_the_last_sequence(dt):
+    """q, k, v cut out of one fused projection, outputs into a larger tensor; rows
+    behind the last sequence are left as they were."""
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    lq = [90, 131]
+    T = sum(lq) + 37
+    qkv = randn(0, T, 8, 64, dtype=dtype)
+    qkv[sum(lq):] = float("nan")
+    q, k, v = qkv[:, :4], qkv[:, 4:6], qkv[:, 6:]
+    rope = lcx.RopeParams("plain", 64)
+    out = torch.full((T, 6, 64), 5.0, dtype=dtype, device="cuda")
+    lse = torch.full((4, T), 5.0, device="cuda")
+    lcx.attn_varlen(q, k, v, lcx.VarlenPlan(lq), rope, out=out[:, 1:5], lse=lse)
+    n = sum(lq)
+    compare(out[:n, 1:5], lse[:, :n], plain(q[:n], k[:n], v[:n], lq, lq, rope), dtype, 131)
+    assert (out[n:] == 5).all() and (lse[:, n:] == 5).all()
+    assert (out[:, 0] == 5).all() and (out[:, 5] == 5).all()
+    o = lcx.attn_varlen(q, k, v, lcx.VarlenPlan(lq), rope)
+    assert (o[n:] == 0).all() and torch.equal(o[:n], out[:n, 1:5])
+
+
+@pytest.mark.parametrize("Hq,H,D,dt", [(4, 2, 64, "bf16"), (8, 2, 128, "bf16"),
+                                       (3, 1, 128, "bf16"), (2, 1, 128, "f32")])
+def test_hidden_nan_and_infinity(Hq, H, D, dt):
+    """NaN and infinity in other sequences, later tokens and tokens behind the window
+    leave a query alone bit for bit; where they are visible they show."""
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    lens = [200, 330]
+    rope = lcx.RopeParams("plain", D)
+    q, k, v = (randn(i, 530, h, D, dtype=dtype) for i, h in ((1, Hq), (2, H), (3, H)))
+    plan = lcx.VarlenPlan(lens)
+    for window, sinks in ((0, 0), (50, 2)):
+        a, la = lcx.attn_varlen(q, k, v, plan, rope, window=window, sinks=sinks, return_lse=True)
+        k2, v2 = k.clone(), v.clone()
+        # token 150 of the first, 100 of the second sequence
+        k2[150], v2[300] = float("nan"), float("inf")
+        v2[150, 0, :7] = float("nan")
+        b, lb = lcx.attn_varlen(q, k2, v2, plan, rope, window=window, sinks=sinks, return_lse=True)
+        sees = torch.zeros(530, dtype=torch.bool, device="cuda")
+        for first, n, t in ((0, 200, 150), (200, 330, 100)):
+            last = n if window == 0 else min(n, t + window)
+            sees[first + t:first + last] = True
+        assert torch.equal(a[~sees], b[~sees]) and torch.equal(la[:, ~sees], lb[:, ~sees])
+        assert not torch.isfinite(b[sees].float()).any()
+        assert torch.isnan(b[150:200 if window == 0 else 200].float()).all()
+        assert (b[200:][sees[200:]] == float("inf")).all()
+        assert torch.equal(la[:, 200:], lb[:, 200:])     # values do not enter the lse
+
+
+def test_nan_value_of_one_column():
+    """A NaN in one column of one visible value reaches that column of the queries
+    that see it, and nothing else."""
+    rope = lcx.RopeParams("plain", 128)
+    q, k, v = (randn(i, 300, h, 128) for i, h in ((1, 4), (2, 2), (3, 2)))
+    plan = lcx.VarlenPlan([300])
+    a = lcx.attn_varlen(q, k, v, plan, rope)
+    v2 = v.clone()
+    v2[140, 1, 77] = float("nan")
+    b = lcx.attn_varlen(q, k, v2, plan, rope)
+    hit = torch.zeros_like(a, dtype=torch.bool)
+    hit[140:, 2:, 77] = True
+    assert torch.isnan(b[hit].float()).all() and torch.equal(a[~hit], b[~hit])
+
+
+def test_long_rows_against_attn_fwd():
+    """Many key tiles: the packed call agrees with attn_fwd per sequence."""
+    rope = lcx.RopeParams("yarn", 128, scale=4.0, original_max_pos=2048)
+    lens = [4000, 1300]
+    q, k, v = (randn(i, 5300, h, 128) for i, h in ((1, 8), (2, 2), (3, 2)))
+    o, lse = lcx.attn_varlen(q, k, v, lcx.VarlenPlan(lens), rope, return_lse=True)
+    a = 0
+    for n in lens:
+        x = [t[a:a + n].transpose(0, 1)[None] for t in (q, k, v)]
+        w, wl = lcx.attn_fwd(*x, rope, return_lse=True)
+        assert (o[a:a + n].float() - w[0].transpose(0, 1).float()).abs().max() <= 4e-2
+        assert (lse[:, a:a + n] - wl[0]).abs().max() <= 2e-2
+        a += n
+
+
+def test_replays_from_a_graph_and_other_streams():
+    rope = lcx.RopeParams("plain", 64)
+    plan = lcx.VarlenPlan([77, 200])
+    q, k, v = (randn(i, 277, h, 64) for i, h in ((1, 4), (2, 2), (3, 2)))
+    k_rot, out = torch.empty_like(k), torch.empty_like(q)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        lcx.attn_varlen(q, k, v, plan, rope, k_rot=k_rot, out=out)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(out, lcx.attn_varlen(q, k, v, plan, rope))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lcx.attn_varlen(q, k, v, plan, rope, k_rot=k_rot, out=out)
+    for i in range(3):
+        for t in (q, k, v):
+            t.copy_(randn(10 * i + t.shape[1], *t.shape))
+        g.replay()
+        assert torch.equal(out, lcx.attn_varlen(q, k, v, plan, rope))
+
+
+def test_a_plan_that_is_not_the_tensors_is_refused():
+    rope = lcx.RopeParams("plain", 64)
+    q, k = randn(0, 10, 2, 64), randn(1, 10, 2, 64)
+    with pytest.raises(lcx.LcxError):
+        lcx.attn_varlen(q, k, k, lcx.VarlenPlan([11]), rope)
+    with pytest.raises(ValueError):
+        lcx.attn_varlen(q, k, k, lcx.VarlenPlan([10], device="cpu"), rope)
