@@ -390,6 +390,9 @@ LCX_API lcx_status lcx_attn_fwd_split_static(const lcx_attn_args *args, int32_t 
  * [0, num_pages) is never followed (its keys count as hidden), and such an
  * entry, a bad sequence number or a lack of pages is reported through the
  * optional dev_status word (written, never cleared) with the entry skipped.
+ * Angles: this section and the next form m * theta'_i from the fp64 frequencies,
+ * lcx_apply_rope and lcx_attn_fwd from lcx_rope_table's fp32 values; at position
+ * m the two differ by at most m theta'_i 2^-24 rad.
  */
 typedef struct {
     void *k_pages, *v_pages;   /* DEVICE [num_layers, num_pages, page_size, Hkv, D]   */
@@ -486,8 +489,7 @@ typedef struct {
 
 /*
  * lcx_paged_append -- rotate the new tokens' keys (times mscale, as
- * lcx_apply_rope does, bit for bit) and write keys and values into their pages
- * of one layer; optionally rotate the tokens' queries in the same pass.  Entry
+ * lcx_apply_rope does) and write keys and values into their pages of one layer; optionally rotate the tokens' queries in the same pass.  Entry
  * i's k-th token sits at position start[i] + k; a position at or beyond the
  * sequence's length is not written (LCX_ERR_INVALID_ARG in the status word:
  * extend first).  Rows of skipped entries and rows outside cu_new are neither

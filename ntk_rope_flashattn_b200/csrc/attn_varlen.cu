@@ -312,7 +312,7 @@ lcx_status varlen_prepare(const lcx_varlen_args *a, VarlenParams &p, bool *noop)
     p.rotate_q = rotate ? 1 : 0;
     p.half = a->rope.pairing == LCX_PAIR_HALF;
     float ms = 1.f;
-    rope_table_unchecked(&a->rope, effective_seq_len(&a->rope, std::max<int64_t>(I.max_k, 1)),
+    rope_freqs_unchecked(&a->rope, effective_seq_len(&a->rope, std::max<int64_t>(I.max_k, 1)),
                          p.theta, &ms);
     const double scale =
         a->softmax_scale > 0.f ? double(a->softmax_scale) : 1.0 / std::sqrt(double(a->D));

@@ -25,6 +25,11 @@ lcx_status check_rope_params(const lcx_rope_params *p);
 void rope_table_unchecked(const lcx_rope_params *p, int64_t seq_len, float *inv_freq,
                           float *mscale);
 
+// The same frequencies before their rounding to fp32 (the packed and paged calls
+// form their angles from these).
+void rope_freqs_unchecked(const lcx_rope_params *p, int64_t seq_len, double *inv_freq,
+                          float *mscale);
+
 // The context length a call uses for the length-dependent modes.
 inline int64_t effective_seq_len(const lcx_rope_params *p, int64_t call_len) {
     return p->seq_len > 0 ? p->seq_len : call_len;

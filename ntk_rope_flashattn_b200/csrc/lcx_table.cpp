@@ -74,7 +74,7 @@ lcx_status check_rope_params(const lcx_rope_params *p) {
     return LCX_OK;
 }
 
-void rope_table_unchecked(const lcx_rope_params *p, int64_t seq_len, float *inv_freq,
+void rope_freqs_unchecked(const lcx_rope_params *p, int64_t seq_len, double *inv_freq,
                           float *mscale) {
     const int D = p->head_dim;
     const double two_pi = 6.283185307179586476925286766559;
@@ -121,11 +121,18 @@ void rope_table_unchecked(const lcx_rope_params *p, int64_t seq_len, float *inv_
                 f = 1.0 / (std::pow(p->base, expo) * lam[i]);
                 break;
         }
-        inv_freq[i] = static_cast<float>(f);
+        inv_freq[i] = f;
     }
     const double ms =
         (mode == LCX_ROPE_YARN && p->scale > 1.0) ? 1.0 + 0.1 * std::log(p->scale) : 1.0;
     *mscale = static_cast<float>(ms);
+}
+
+void rope_table_unchecked(const lcx_rope_params *p, int64_t seq_len, float *inv_freq,
+                          float *mscale) {
+    double f[256];   // head_dim <= 512
+    rope_freqs_unchecked(p, seq_len, f, mscale);
+    for (int i = 0; i < p->head_dim / 2; ++i) inv_freq[i] = static_cast<float>(f[i]);
 }
 
 }  // namespace lcx

@@ -4,7 +4,9 @@
 //
 // y_p = ms (x_p cos phi - x_q sin phi), y_q = ms (x_p sin phi + x_q cos phi),
 // phi = m theta'_i, as in apply_rope.cu, with m the token's position in its own
-// sequence ("Long Context: RoPE / YaRN / NTK / MLA", 2.2, 2.4, 6.4).
+// sequence ("Long Context: RoPE / YaRN / NTK / MLA", 2.2, 2.4, 6.4).  The angles
+// come from the fp64 frequencies: the fp32 table's rounding would move the angle
+// at m = 65536 by up to m 2^-25 = 0.002 rad, which fp32 caches can tell.
 //
 // Bound by HBM: each input vector is read and each output vector written once.
 // A CTA owns rows_per_cta tokens and a slice of the heads; one thread owns one
@@ -37,7 +39,7 @@ struct AppendParams {
     int n, T, Hq, Hkv, S, MP, P, ps_log2;
     int D, jobs, rows, slices, per;     // jobs per token; tokens per CTA; head slices, heads each
     float ms;
-    float theta[64];
+    double theta[64];
 };
 
 // Where a token goes: its position and its page's (page << ps_log2 | slot), or
@@ -237,7 +239,7 @@ lcx_status rotate_packed(const lcx_rope_params *rope, int64_t seq_len, const voi
     a.T = int(T);
     a.Hkv = int(H);
     a.D = int(D);
-    rope_table_unchecked(rope, effective_seq_len(rope, seq_len), a.theta, &a.ms);
+    rope_freqs_unchecked(rope, effective_seq_len(rope, seq_len), a.theta, &a.ms);
     return launch_append(a, dtype == LCX_BF16 ? 2 : 4, rope->pairing == LCX_PAIR_HALF, s);
 }
 
@@ -306,7 +308,7 @@ extern "C" lcx_status lcx_paged_append(const lcx_paged_cache *cache,
     a.P = p.P;
     a.ps_log2 = p.ps_log2;
     a.D = p.D;
-    rope_table_unchecked(&g->rope, g->rope.seq_len, a.theta, &a.ms);
+    rope_freqs_unchecked(&g->rope, g->rope.seq_len, a.theta, &a.ms);
     return launch_append(a, p.es, g->rope.pairing == LCX_PAIR_HALF,
                          static_cast<cudaStream_t>(stream));
 }

@@ -32,7 +32,7 @@ struct DecodeParams {
     long long window, sinks;
     int rotate, half;
     float c_log2;               // logit scale in log2 units
-    float theta[64];
+    double theta[64];
 };
 
 template <typename T>
@@ -223,7 +223,7 @@ extern "C" lcx_status lcx_paged_decode(const lcx_paged_cache *cache,
     p.rotate = (g->flags & LCX_DECODE_PREROTATED) || g->rope.mode == LCX_ROPE_NONE ? 0 : 1;
     p.half = g->rope.pairing == LCX_PAIR_HALF;
     float ms = 1.f;
-    rope_table_unchecked(&g->rope, g->rope.seq_len, p.theta, &ms);
+    rope_freqs_unchecked(&g->rope, g->rope.seq_len, p.theta, &ms);
     const double scale =
         g->softmax_scale > 0.f ? double(g->softmax_scale) : 1.0 / std::sqrt(double(c.D));
     p.c_log2 = float(scale * (p.rotate ? double(ms) : 1.0) * 1.4426950408889634);

@@ -23,8 +23,22 @@ __device__ __forceinline__ float rope_reduced_angle(long long m, float theta) {
     return static_cast<float>(r);
 }
 
+// The same for a frequency in fp64: the product is rounded once (2^-53 of the
+// angle), so positions up to 2^30 keep the angle to 2^-23 rad before the rounding
+// to fp32.
+__device__ __forceinline__ float rope_reduced_angle(long long m, double theta) {
+    const double phi = static_cast<double>(m) * theta;
+    const double k = rint(phi * kInvTwoPi);
+    double r = fma(-k, kTwoPiHi, phi);
+    r = fma(-k, kTwoPiLo, r);
+    return static_cast<float>(r);
+}
+
 // Accurate (libm) cosine and sine of m * theta.
 __device__ __forceinline__ void rope_sincos(long long m, float theta, float *c, float *s) {
+    sincosf(rope_reduced_angle(m, theta), s, c);
+}
+__device__ __forceinline__ void rope_sincos(long long m, double theta, float *c, float *s) {
     sincosf(rope_reduced_angle(m, theta), s, c);
 }
 

@@ -41,7 +41,7 @@ struct VarlenParams {
     int rotate_q, half;
     float c_log2;                           // logit scale in log2 units
     unsigned long long timeout_ns;
-    float theta[64];
+    double theta[64];
 };
 
 // The unit as the plan holds it, or one without rows when it does not fit the

@@ -20,9 +20,11 @@ U_OUT = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
 
 
 def table64(rope):
-    """(theta'_i, mscale) as the library rounds them to fp32."""
-    import ntk_rope_flashattn_b200 as lcx
-    t, ms = lcx.rope_table(rope)
+    """(theta'_i, mscale) in 64 bits."""
+    import oracle
+    t, ms = oracle.rope_theta_ext(rope.mode, rope.head_dim, rope.base, rope.scale,
+                                  rope.original_max_pos, rope.alpha, rope.beta,
+                                  seq_len=rope.seq_len)
     return torch.from_numpy(t).double(), float(ms)
 
 

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import ntk_rope_flashattn_b200 as lcx
-from serving_plain import attend, check, rotate
+from serving_plain import U_OUT, attend, check, rotate
 
 pytestmark = pytest.mark.gpu
 
@@ -230,9 +230,9 @@ def test_decode_on_another_stream_with_its_own_workspace():
                                               (128, 8, 32, 16, "bf16", True),
                                               (64, 4, 4, 1, "f32", False),
                                               (128, 2, 10, 64, "f32", True)])
-def test_append_equals_apply_rope(D, H, Hq, ps, dt, nhd, pairing):
-    """Keys land in their pages exactly as apply_rope rotates them, values as they
-    are, and nothing else is touched."""
+def test_append_rotates_and_places(D, H, Hq, ps, dt, nhd, pairing):
+    """Keys land in their pages rotated (within one rounding of the 64-bit rotation,
+    and equal to the packed copy), values as they are, and nothing else is touched."""
     dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
     rope = lcx.RopeParams("yarn", D, scale=8.0, original_max_pos=512, pairing=pairing)
     old, new = [30, 0, 7, 511], [1, 40, 0, 130]
@@ -264,10 +264,14 @@ def test_append_equals_apply_rope(D, H, Hq, ps, dt, nhd, pairing):
             continue
         r = slice(cu[i], cu[i + 1])
         p0 = int(start[i])
-        for x, w in ((q, wq), (k, wk)):
-            w[r] = lcx.apply_rope(x[r].transpose(0, 1)[None].contiguous(), rope,
-                                  pos_offset=p0)[0].transpose(0, 1)
         pos = torch.arange(p0, p0 + cnt[i], device="cuda")
+        for x, w, got in ((q, wq, q_out), (k, wk, k_out)):
+            exact = rotate(x[r].cpu(), pos.cpu(), rope)
+            # one output rounding; the angle, its cos/sin and mscale within 2^-22 each,
+            # times the pair's length (at most sqrt(2) max|x| mscale)
+            tol = U_OUT[dtype] * exact.abs() + 8 * 2.0 ** -22 * float(x.abs().max())
+            assert ((got[r].double().cpu() - exact).abs() <= tol).all()
+            w[r] = got[r]
         pg, sl = c.block_table[s].long()[pos // ps], pos % ps
         kp[1, pg, sl], vp[1, pg, sl] = wk[r], v[r]
     assert torch.equal(c.k_pages, kp) and torch.equal(c.v_pages, vp)
