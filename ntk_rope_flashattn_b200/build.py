@@ -19,7 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["lcx_table.cpp", "apply_rope.cu", "attn_fwd.cu", "merge.cu", "static_scratch.cu",
            "pages.cu", "paged_append.cu", "paged_decode.cu", "attn_varlen.cu"]
-HEADERS = ["lcx_internal.h", "sm100.cuh", "rope_angle.cuh", "vec16.cuh", "paged.cuh", "varlen.cuh"]
+HEADERS = ["lcx_internal.h", "sm100.cuh", "rope_angle.cuh", "vec16.cuh", "paged.cuh",
+           "varlen.cuh", "mma_sync.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-Xcompiler", "-fvisibility=hidden", "-I", INCLUDE]

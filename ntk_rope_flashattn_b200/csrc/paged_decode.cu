@@ -3,19 +3,67 @@
 //
 // o = sum_j softmax_j(c <q', k'_j>) v_j over the visible keys, evaluated with a
 // running maximum and sum ("8.3 长上下文技术", 8.3.4), q' = q rotated at the
-// token's position.  Bound by HBM: every visible key and value is read once.
+// token's position; parts over disjoint keys join by rescaling with their maxima
+// (8.3.5 step 3).
+//
+// Bound by HBM: every visible key and value is read once, 4 Hkv D bytes per key
+// (bf16) against 4 Hq D flops.
+//
+// Work: the visible keys of each (entry, kv head, block of query heads), a
+// "segment", are cut into blocks of 32 to 128 keys; the blocks of all segments in
+// order form one list, and every CTA takes an equal stretch of it, so a batch of
+// ragged lengths loads the SMs evenly without a plan from the host (lengths are
+// device data).  A CTA sees at most two segments whose other blocks lie in other
+// CTAs, its first and its last: their parts go to the workspace and a second
+// kernel joins them, in CTA order; whole segments are written at once.
+//
+// Inside a CTA each of the four warps takes a quarter of every block and keeps a
+// ring of its own: cp.async copies (16 bytes, any page size and strides, hidden
+// keys zero-filled) run two tiles ahead without a barrier between warps, across
+// segment borders.  Two CTAs per SM keep 128 KB in flight.
+//
+// Products: mma.sync with the query heads as the 16 rows.  With at most 8 heads
+// the rows hold two bf16 parts of q' (hi in rows 0-7, lo in 8-15) and later of the
+// weights, which costs nothing (the rows would be empty) and keeps 16 bits; with 9
+// to 16 heads (kWide) q' takes a second product and the weights are rounded to
+// bf16.  fp32 pools use tf32 products with two parts of every operand.
 #include <algorithm>
 #include <cmath>
 
+#include "mma_sync.cuh"
 #include "paged.cuh"
 #include "rope_angle.cuh"
+#include "sm100.cuh"
 #include "vec16.cuh"
 
 namespace lcx {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kGB = 8;          // query heads a CTA serves
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kStages = 3;      // ring of a warp: one tile in use, two in flight
+constexpr int kHalf = 4096;     // bytes of a tile's keys, and of its values
+
+template <typename T, int D, bool kWide>
+struct Dec {
+    static constexpr int ES = sizeof(T);
+    static constexpr int ROW = D * ES;            // bytes of a key row
+    static constexpr int KT = kHalf / ROW;        // keys of a warp's tile
+    static constexpr int BLK = KT * kWarps;       // keys of a block
+    static constexpr int HB = kWide ? 16 : 8;     // query heads of a segment
+    static constexpr int CPR = ROW / 16;          // 16-byte chunks of a row
+    static constexpr int RPI = 32 / CPR;          // rows a warp copies per instruction
+    static constexpr int NI = KT / RPI;
+    static_assert(!kWide || ES == 2, "wide segments: 16-bit pools");
+    // shared memory: rings, q', the warps' outputs (8 heads x 64 columns at a
+    // time), their statistics, the rings' visibility masks
+    static constexpr int kOffQ = kWarps * kStages * 2 * kHalf;
+    static constexpr int kBytesQ = 8192;
+    static constexpr int kOffO = kOffQ + kBytesQ;
+    static constexpr int kOffM = kOffO + kWarps * 8 * 64 * 4;
+    static constexpr int kOffMask = kOffM + kWarps * 16 * 2 * 4;
+    static constexpr int kSmem = kOffMask + kWarps * kStages * 4 + 16;
+    static_assert(kSmem <= 115712, "two CTAs per SM");
+};
 
 struct DecodeParams {
     const char *q;
@@ -29,122 +77,674 @@ struct DecodeParams {
     long long qs[2], os[2];     // token, head
     int n, Hq, Hkv, G, hb;      // hb: head blocks of a kv head
     int S, MP, P, ps_log2;
-    long long window, sinks;
+    int window, sinks;
     int rotate, half;
     float c_log2;               // logit scale in log2 units
+    int ctas, blk;              // CTAs of the attention kernel, keys per block
+    float *part_o, *part_ml;    // [2 ctas][HB][D], [2 ctas][HB][2]
     double theta[64];
 };
 
-template <typename T>
-__device__ __forceinline__ float ld(const T *p) {
-    return static_cast<float>(*p);
+// The visible keys of an entry: [0, ns) and [lo, len).
+struct Entry {
+    int id, len, ns, lo, nvis, nblk;
+};
+__device__ __forceinline__ Entry load_entry(const DecodeParams &p, int e, bool report) {
+    Entry x;
+    x.id = p.ids[e];
+    x.len = 0;
+    bool bad = x.id >= p.S;
+    if (x.id >= 0 && !bad) {
+        const long long most = (long long)p.MP << p.ps_log2;
+        const int len = p.lens[x.id];
+        bad = len < 0 || len > most;
+        x.len = len < 0 ? 0 : int(min((long long)len, most));
+    }
+    if (bad && report) raise_status(p.status, LCX_ERR_INVALID_ARG);
+    x.lo = p.window > 0 ? max(0, x.len - p.window) : 0;
+    x.ns = min(p.sinks, x.lo);
+    x.nvis = x.len - x.lo + x.ns;
+    x.nblk = max(1, (x.nvis + p.blk - 1) / p.blk);   // an empty entry writes its zeros
+    return x;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32)
+// Sum of x over the CTA's threads (4 warps); scratch of 4 ints.
+__device__ __forceinline__ int cta_sum(int x, int *scratch) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = x;
+    __syncthreads();
+    return scratch[0] + scratch[1] + scratch[2] + scratch[3];
+}
+
+// First block of CTA c's stretch of the list of nb blocks.
+__device__ __forceinline__ long long stretch(long long nb, int c, int ctas) {
+    return nb * c / ctas;
+}
+
+// Position in the block list: block blk of segment (entry e, head block r).
+struct Cursor {
+    int e, r, blk;
+    Entry x;
+    __device__ __forceinline__ bool last() const { return blk == x.nblk - 1; }
+    __device__ __forceinline__ void next(const DecodeParams &p) {
+        if (++blk < x.nblk) return;
+        blk = 0;
+        if (++r < p.Hkv * p.hb) return;
+        r = 0;
+        if (++e < p.n) x = load_entry(p, e, false);
+    }
+};
+
+// 16-byte chunk c of row r of a tile with CPR chunks per row, moved so that the
+// reads below touch every bank once: 16-bit rows by ldmatrix (8 rows, one chunk);
+// fp32 keys by rows r, r + 1 and four chunks, fp32 values by every other row.
+template <typename T, int CPR>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c, bool value) {
+    if constexpr (sizeof(T) == 2)
+        return (r * CPR + (c ^ (r & 7))) * 16;
+    else
+        return (r * CPR + (c ^ (value ? ((r >> 1) & 3) << 1 : (r & 1) << 2))) * 16;
+}
+
+// x in two tf32 parts (an infinite x has no second part).
+__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
+    const float h = round_tf32(x);
+    float l = x - h;
+    l = l == l ? l : 0.f;
+    hi = __float_as_uint(h);
+    lo = __float_as_uint(round_tf32(l));
+}
+// Two values in two bf16 parts each, packed.
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = pk(x, y);
+    lo = pk(x - bf16lo_to_f32(hi), y - bf16hi_to_f32(hi));
+}
+// hi + lo where lo is a correction: an infinite or NaN hi stands alone.
+__device__ __forceinline__ float join(float hi, float lo) {
+    return fabsf(hi) < INFINITY ? hi + lo : hi;
+}
+
+// ------------------------------------------------------------------ kernel
+template <typename T, int D, bool kWide>
+__global__ void __launch_bounds__(kThreads, 2)
     paged_decode_kernel(const __grid_constant__ DecodeParams p) {
-    constexpr int E = D / 32;   // dims per lane: lane, lane + 32, ..
-    __shared__ float sq[kGB][D];
-    __shared__ float sm[kWarps][kGB], sl[kWarps][kGB], so[kWarps][kGB][D];
+    using C = Dec<T, D, kWide>;
+    extern __shared__ __align__(128) uint8_t sm[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int e = blockIdx.x / (p.Hkv * p.hb), r = blockIdx.x % (p.Hkv * p.hb);
-    const int kvh = r / p.hb, h0 = kvh * p.G + (r % p.hb) * kGB;
-    const int nh = min(kGB, (kvh + 1) * p.G - h0);
-    const int id = p.ids[e];
-    int len = 0;
-    if (id >= p.S) {
-        if (threadIdx.x == 0) raise_status(p.status, LCX_ERR_INVALID_ARG);
-    } else if (id >= 0) {
-        len = p.lens[id];
-        const long long most = (long long)p.MP << p.ps_log2;
-        if (len < 0 || len > most) {
-            if (threadIdx.x == 0) raise_status(p.status, LCX_ERR_INVALID_ARG);
-            len = int(min(max((long long)len, 0ll), most));
-        }
-    }
-    // q' of the block's heads, fp32
-    for (int i = threadIdx.x; i < nh * (D / 2); i += kWarps * 32) {
-        const int h = i / (D / 2), pr = i % (D / 2);
-        const T *src = reinterpret_cast<const T *>(p.q) + e * p.qs[0] + (h0 + h) * p.qs[1];
-        const int a = p.half ? pr : 2 * pr, b = p.half ? pr + D / 2 : 2 * pr + 1;
-        float x = ld(src + a), y = ld(src + b), c = 1.f, s = 0.f;
-        if (p.rotate) rope_sincos(len - 1, p.theta[pr], &c, &s);
-        sq[h][a] = x * c - y * s;
-        sq[h][b] = x * s + y * c;
-    }
-    __syncthreads();
-    float m[kGB], l[kGB], acc[kGB][E];
+    const int g = lane >> 2, c4 = lane & 3;
+    uint8_t *ring = sm + warp * kStages * 2 * kHalf;
+    uint32_t *mask = reinterpret_cast<uint32_t *>(sm + C::kOffMask) + warp * kStages;
+    float *sO = reinterpret_cast<float *>(sm + C::kOffO);     // [warp][8][64]
+    float *sM = reinterpret_cast<float *>(sm + C::kOffM);     // [warp][16][2]
+    const int R = p.Hkv * p.hb;
+    pdl_launch_dependents();   // the join may be scheduled; it waits for this grid
+
+    // This CTA's stretch [b0, b1) of the block list, and where it starts.
+    int *scan = reinterpret_cast<int *>(sO);
+    Cursor L;
+    int nb = 0;
+    {
+        int mine = 0;
+        for (int e = threadIdx.x; e < p.n; e += kThreads)
+            mine += load_entry(p, e, blockIdx.x == 0).nblk;
+        const long long all = (long long)cta_sum(mine, scan) * R;
+        const long long b0 = stretch(all, blockIdx.x, p.ctas);
+        nb = int(stretch(all, blockIdx.x + 1, p.ctas) - b0);
+        if (nb == 0) return;
+        // the entry that holds b0: prefix sums, 128 entries at a time
+        long long before = 0;          // blocks per head block of the entries before
+        int base = 0;
+        for (;; base += kThreads) {
+            const int e = base + threadIdx.x;
+            const int here = e < p.n ? load_entry(p, e, false).nblk : 0;
+            int incl = here;
 #pragma unroll
-    for (int h = 0; h < kGB; ++h) {
-        m[h] = -INFINITY;
-        l[h] = 0.f;
-#pragma unroll
-        for (int x = 0; x < E; ++x) acc[h][x] = 0.f;
-    }
-    for (int j = warp; j < len; j += kWarps) {
-        if (p.window > 0 && len - 1 - j >= p.window && j >= p.sinks) continue;
-        const int page = p.table[(long long)id * p.MP + (j >> p.ps_log2)];
-        if (page < 0 || page >= p.P) {
-            if (lane == 0) raise_status(p.status, LCX_ERR_INVALID_ARG);
-            continue;
-        }
-        const int slot = j & ((1 << p.ps_log2) - 1);
-        const T *k = reinterpret_cast<const T *>(p.kp) + page * p.ks[0] + slot * p.ks[1] +
-                     kvh * p.ks[2];
-        const T *v = reinterpret_cast<const T *>(p.vp) + page * p.vs[0] + slot * p.vs[1] +
-                     kvh * p.vs[2];
-        float kx[E], vx[E];
-#pragma unroll
-        for (int x = 0; x < E; ++x) {
-            kx[x] = ld(k + lane + 32 * x);
-            vx[x] = ld(v + lane + 32 * x);
-        }
-#pragma unroll
-        for (int h = 0; h < kGB; ++h) {
-            if (h >= nh) break;
-            float d = 0.f;
-#pragma unroll
-            for (int x = 0; x < E; ++x) d = fmaf(sq[h][lane + 32 * x], kx[x], d);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-            d *= p.c_log2;
-            const float mn = fmaxf(m[h], d);
-            const float al = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mn);
-            const float w = d == -INFINITY ? 0.f : exp2f(d - mn);
-            m[h] = mn;
-            l[h] = l[h] * al + w;
-#pragma unroll
-            for (int x = 0; x < E; ++x) acc[h][x] = acc[h][x] * al + w * vx[x];
-        }
-    }
-#pragma unroll
-    for (int h = 0; h < kGB; ++h) {
-        if (h >= nh) break;
-        if (lane == 0) {
-            sm[warp][h] = m[h];
-            sl[warp][h] = l[h];
-        }
-#pragma unroll
-        for (int x = 0; x < E; ++x) so[warp][h][lane + 32 * x] = acc[h][x];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < nh * D; i += kWarps * 32) {
-        const int h = i / D, d = i % D;
-        float mx = -INFINITY, z = 0.f, o = 0.f;
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm[w][h]);
-        if (mx != -INFINITY)
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = exp2f(sm[w][h] - mx);
-                z += f * sl[w][h];
-                o += f * so[w][h][d];
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
             }
-        const float out = z == 0.f ? 0.f : o / z;   // a NaN sum stays NaN
-        T *dst = reinterpret_cast<T *>(p.o) + e * p.os[0] + (h0 + h) * p.os[1];
-        dst[d] = static_cast<T>(out);
-        if (p.lse && d == 0)
+            __syncthreads();
+            if (lane == 31) scan[warp] = incl;
+            if (threadIdx.x == 0) scan[4] = -1;
+            __syncthreads();
+            for (int w = 0; w < warp; ++w) incl += scan[w];
+            const long long end = before + incl;
+            if (here > 0 && end * R > b0 && (end - here) * R <= b0) {
+                scan[4] = e;
+                scan[5] = int(b0 - (end - here) * R);
+            }
+            before += scan[0] + scan[1] + scan[2] + scan[3];
+            __syncthreads();
+            if (scan[4] >= 0 || base + kThreads >= p.n) break;
+        }
+        L.e = scan[4];
+        const int off = scan[5];
+        __syncthreads();
+        if (L.e < 0) return;           // not reached: b0 < all
+        L.x = load_entry(p, L.e, false);
+        L.r = off / L.x.nblk;
+        L.blk = off % L.x.nblk;
+    }
+    Cursor W = L;                      // the tile in use; L the next tile to copy
+    int first_blk = W.blk;             // first block of the current segment here
+
+    // Page and slot of this lane's key of the tile at L, loaded one tile early so
+    // that the copies do not wait for the table.
+    int page = -1, slot = 0;
+    auto lookup = [&]() {
+        const int v = L.blk * C::BLK + warp * C::KT + lane;
+        page = -1;
+        if (lane < C::KT && v < L.x.nvis) {
+            const int key = v < L.x.ns ? v : L.x.lo + (v - L.x.ns);
+            page = __ldg(p.table + (long long)L.x.id * p.MP + (key >> p.ps_log2));
+            slot = key & ((1 << p.ps_log2) - 1);
+        }
+    };
+    int to_copy = nb;
+    lookup();
+    auto copy_tile = [&](int stage) {
+        if (to_copy > 0) {
+            const int v = L.blk * C::BLK + warp * C::KT + lane;
+            if (lane < C::KT && v < L.x.nvis && (page < 0 || page >= p.P)) {
+                page = -1;
+                raise_status(p.status, LCX_ERR_INVALID_ARG);
+            }
+            const uint32_t seen = __ballot_sync(0xffffffffu, page >= 0);
+            const int kvh = L.r / p.hb;
+            const uint32_t dst = smem_u32(ring + stage * 2 * kHalf);
+            const int c = lane % C::CPR;
+#pragma unroll
+            for (int i = 0; i < C::NI; ++i) {
+                const int r = i * C::RPI + lane / C::CPR;
+                const int pg = __shfl_sync(0xffffffffu, page, r);
+                const int sl = __shfl_sync(0xffffffffu, slot, r);
+                const int bytes = pg >= 0 ? 16 : 0;
+                const long long a = max(pg, 0);
+                const char *k = p.kp + (a * p.ks[0] + sl * p.ks[1] + kvh * p.ks[2]) * C::ES + 16 * c;
+                const char *w = p.vp + (a * p.vs[0] + sl * p.vs[1] + kvh * p.vs[2]) * C::ES + 16 * c;
+                cp_async16(dst + chunk_at<T, C::CPR>(r, c, false), bytes ? k : p.kp, bytes);
+                cp_async16(dst + kHalf + chunk_at<T, C::CPR>(r, c, true), bytes ? w : p.vp, bytes);
+            }
+            if (lane == 0) mask[stage] = seen;
+            if (--to_copy > 0) {
+                L.next(p);
+                lookup();
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) copy_tile(s);
+
+    constexpr int NT = D / 8;          // output column tiles
+    constexpr int QF = C::ES == 2 ? (kWide ? 1 : D / 16) : D / 8;
+    uint32_t qf[QF][4];                // q' as A fragments (wide: read per tile)
+    float acc[NT][4];
+    float m[2], l[2];                  // rows g and g + 8 (narrow: row g alone)
+    const uint32_t sq = smem_u32(sm + C::kOffQ);
+
+    int stage = 0;
+    for (int b = 0; b < nb; ++b) {
+        if (b == 0 || W.blk == 0) {
+            // -------------------------------------------------- a segment starts
+            first_blk = W.blk;
+            const int kvh = W.r / p.hb, h0 = kvh * p.G + (W.r % p.hb) * C::HB;
+            const int nh = min(C::HB, (kvh + 1) * p.G - h0);
+            const T *q = reinterpret_cast<const T *>(p.q) + W.e * p.qs[0];
+            // one thread per pair; the heads share its angle
+            for (int pr = threadIdx.x % (D / 2); pr < D / 2; pr += kThreads) {
+                constexpr int kStep = kThreads / (D / 2);
+                const int a = p.half ? pr : 2 * pr, b2 = p.half ? pr + D / 2 : 2 * pr + 1;
+                float cs = 1.f, sn = 0.f;
+                if (p.rotate) rope_sincos(W.x.len - 1, p.theta[pr], &cs, &sn);
+#pragma unroll 4
+                for (int h = threadIdx.x / (D / 2); h < C::HB; h += kStep) {
+                    float x = 0.f, y = 0.f;
+                    if (h < nh) {
+                        x = static_cast<float>(q[(h0 + h) * p.qs[1] + a]);
+                        y = static_cast<float>(q[(h0 + h) * p.qs[1] + b2]);
+                    }
+                    const float u = x * cs - y * sn, w = x * sn + y * cs;
+                    if constexpr (C::ES == 2) {
+                        // rows h (hi) and HB + h (lo), chunks swizzled
+                        auto put = [&](int col, float z) {
+                            const uint32_t hi = pk(z, 0.f);
+                            const float zl = z - bf16lo_to_f32(hi);
+                            const uint32_t lo = pk(zl == zl ? zl : 0.f, 0.f);
+                            const int chunk = col >> 3, in = (col & 7) * 2;
+                            auto at = [&](int row) {
+                                return reinterpret_cast<uint16_t *>(
+                                    sm + C::kOffQ + row * C::ROW +
+                                    ((chunk ^ (row & 7)) << 4) + in);
+                            };
+                            *at(h) = uint16_t(hi);
+                            *at(C::HB + h) = uint16_t(lo);
+                        };
+                        put(a, u);
+                        put(b2, w);
+                    } else {
+                        uint32_t *s = reinterpret_cast<uint32_t *>(sm + C::kOffQ);
+                        split_tf32(u, s[h * D + a], s[(8 + h) * D + a]);
+                        split_tf32(w, s[h * D + b2], s[(8 + h) * D + b2]);
+                    }
+                }
+            }
+            __syncthreads();
+            if constexpr (C::ES == 2 && !kWide) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const int row = lane & 15, chunk = 2 * k + (lane >> 4);
+                    ldmatrix4(qf[k], sq + row * C::ROW + ((chunk ^ (row & 7)) << 4));
+                }
+            } else if constexpr (C::ES == 4) {
+                // k slots c4 and c4 + 4 of step 2 i + j hold columns 16 i + 4 c4 + 2 j
+                // and that + 1, the order in which a key's 16-byte reads arrive
+                const uint32_t *s = reinterpret_cast<const uint32_t *>(sm + C::kOffQ);
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k) {
+                    const int col = 16 * (k >> 1) + 4 * c4 + 2 * (k & 1);
+                    qf[k][0] = s[g * D + col];
+                    qf[k][1] = s[(8 + g) * D + col];
+                    qf[k][2] = s[g * D + col + 1];
+                    qf[k][3] = s[(8 + g) * D + col + 1];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m[i] = -INFINITY;
+                l[i] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+        }
+        // ------------------------------------------------------ one tile
+        cp_async_wait<kStages - 2>();
+        __syncwarp();
+        const uint32_t seen = mask[stage];
+        const uint32_t kb = smem_u32(ring + stage * 2 * kHalf), vb = kb + kHalf;
+        constexpr int NS = C::KT / 8;      // score tiles of 8 keys
+        float s[NS][4];
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[j][i] = 0.f;
+        if constexpr (C::ES == 2) {
+            float s2[kWide ? NS : 1][4];
+            if constexpr (kWide) {
+#pragma unroll
+                for (int j = 0; j < NS; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s2[j][i] = 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < D / 16; k += 2) {
+                uint32_t a0[4], a1[4], l0[4], l1[4];
+                if constexpr (kWide) {
+                    const int row = lane & 15, hc = lane >> 4;
+                    auto at = [&](int r, int chunk) {
+                        return sq + r * C::ROW + ((chunk ^ (r & 7)) << 4);
+                    };
+                    ldmatrix4(a0, at(row, 2 * k + hc));
+                    ldmatrix4(a1, at(row, 2 * k + 2 + hc));
+                    ldmatrix4(l0, at(16 + row, 2 * k + hc));
+                    ldmatrix4(l1, at(16 + row, 2 * k + 2 + hc));
+                }
+#pragma unroll
+                for (int j = 0; j < NS; ++j) {
+                    uint32_t kf[4];        // 8 keys x 32 columns
+                    ldmatrix4(kf, kb + chunk_at<T, C::CPR>(8 * j + (lane & 7), 2 * k + (lane >> 3),
+                                                           false));
+                    if constexpr (kWide) {
+                        mma_bf16(s[j], a0, kf[0], kf[1]);
+                        mma_bf16(s2[j], l0, kf[0], kf[1]);
+                        mma_bf16(s[j], a1, kf[2], kf[3]);
+                        mma_bf16(s2[j], l1, kf[2], kf[3]);
+                    } else {
+                        mma_bf16(s[j], qf[k], kf[0], kf[1]);
+                        mma_bf16(s[j], qf[k + 1], kf[2], kf[3]);
+                    }
+                }
+            }
+            if constexpr (kWide) {
+#pragma unroll
+                for (int j = 0; j < NS; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[j][i] = join(s[j][i], s2[j][i]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    float4 x;
+                    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                                 : "r"(kb + chunk_at<T, C::CPR>(8 * j + g, 4 * i + c4, false))
+                                 : "memory");
+                    uint32_t h[4], w[4];
+                    split_tf32(x.x, h[0], w[0]);
+                    split_tf32(x.y, h[1], w[1]);
+                    split_tf32(x.z, h[2], w[2]);
+                    split_tf32(x.w, h[3], w[3]);
+                    mma_tf32(s[j], qf[2 * i], w[0], w[1]);
+                    mma_tf32(s[j], qf[2 * i + 1], w[2], w[3]);
+                    mma_tf32(s[j], qf[2 * i], h[0], h[1]);
+                    mma_tf32(s[j], qf[2 * i + 1], h[2], h[3]);
+                }
+        }
+        // scores of keys 8 j + 2 c4 + {0, 1}: row g in s[j][0..1], row g + 8 in
+        // s[j][2..3] (narrow: the second part of row g)
+        constexpr int NR = kWide ? 2 : 1;
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool in = (seen >> (8 * j + 2 * c4 + i)) & 1;
+                if constexpr (kWide) {
+                    s[j][i] = in ? s[j][i] * p.c_log2 : -INFINITY;
+                    s[j][i + 2] = in ? s[j][i + 2] * p.c_log2 : -INFINITY;
+                } else {
+                    s[j][i] = in ? join(s[j][i], s[j][i + 2]) * p.c_log2 : -INFINITY;
+                }
+            }
+        float mref[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            float mx = m[r];
+#pragma unroll
+            for (int j = 0; j < NS; ++j) mx = fmaxf(mx, fmaxf(s[j][2 * r], s[j][2 * r + 1]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            mref[r] = mx;
+        }
+        bool grew = mref[0] > m[0];
+        if constexpr (kWide) grew |= mref[1] > m[1];
+        if (__any_sync(0xffffffffu, grew)) {
+            float al[2];
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                al[r] = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - mref[r]);
+                m[r] = mref[r];
+                l[r] *= al[r];
+            }
+            if constexpr (!kWide) al[1] = al[0];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                acc[j][0] *= al[0];
+                acc[j][1] *= al[0];
+                acc[j][2] *= al[1];
+                acc[j][3] *= al[1];
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < NR; ++r) mref[r] = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                s[j][2 * r] = ex2_approx(s[j][2 * r] - mref[r]);
+                s[j][2 * r + 1] = ex2_approx(s[j][2 * r + 1] - mref[r]);
+                l[r] += s[j][2 * r] + s[j][2 * r + 1];
+            }
+        if constexpr (C::ES == 2) {
+#pragma unroll
+            for (int j = 0; j < NS; j += 2) {
+                uint32_t a[4];
+                if constexpr (kWide) {
+                    a[0] = pk(s[j][0], s[j][1]);
+                    a[1] = pk(s[j][2], s[j][3]);
+                    a[2] = pk(s[j + 1][0], s[j + 1][1]);
+                    a[3] = pk(s[j + 1][2], s[j + 1][3]);
+                } else {
+                    split_bf16(s[j][0], s[j][1], a[0], a[1]);
+                    split_bf16(s[j + 1][0], s[j + 1][1], a[2], a[3]);
+                }
+#pragma unroll
+                for (int t = 0; t < NT; t += 2) {
+                    uint32_t vf[4];        // 16 keys x 16 columns
+                    ldmatrix4_trans(vf, vb + chunk_at<T, C::CPR>(8 * j + (lane & 15),
+                                                                 t + (lane >> 4), true));
+                    mma_bf16(acc[t], a, vf[0], vf[1]);
+                    mma_bf16(acc[t + 1], a, vf[2], vf[3]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+                // k slots c4 and c4 + 4 hold keys 2 c4 and 2 c4 + 1
+                uint32_t a[4];
+                split_tf32(s[j][0], a[0], a[1]);
+                split_tf32(s[j][1], a[2], a[3]);
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    // columns 32 i + 4 g + {0..3}: one per output tile 4 i + {0..3}
+                    float x[2][4];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                     : "=f"(x[k][0]), "=f"(x[k][1]), "=f"(x[k][2]), "=f"(x[k][3])
+                                     : "r"(vb + chunk_at<T, C::CPR>(8 * j + 2 * c4 + k, 8 * i + g,
+                                                                    true))
+                                     : "memory");
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        uint32_t h0, w0, h1, w1;
+                        split_tf32(x[0][t], h0, w0);
+                        split_tf32(x[1][t], h1, w1);
+                        mma_tf32(acc[4 * i + t], a, w0, w1);
+                        mma_tf32(acc[4 * i + t], a, h0, h1);
+                    }
+                }
+            }
+        }
+        __syncwarp();                      // the tile is read: its stage may be refilled
+        copy_tile((stage + kStages - 1) % kStages);
+        stage = (stage + 1) % kStages;
+
+        if (W.last() || b == nb - 1) {
+            // -------------------------------------------------- a segment ends here
+            const bool whole = first_blk == 0 && W.last();
+            const int kvh = W.r / p.hb, h0 = kvh * p.G + (W.r % p.hb) * C::HB;
+            const int nh = min(C::HB, (kvh + 1) * p.G - h0);
+            // the stretch's first segment, or a later one that runs past its end
+            const int part = 2 * blockIdx.x + (b - (W.blk - first_blk) > 0 ? 1 : 0);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+            }
+            if (c4 == 0) {
+                sM[(warp * 16 + g) * 2] = m[0];
+                sM[(warp * 16 + g) * 2 + 1] = l[0];
+                if constexpr (kWide) {
+                    sM[(warp * 16 + 8 + g) * 2] = m[1];
+                    sM[(warp * 16 + 8 + g) * 2 + 1] = l[1];
+                }
+            }
+#pragma unroll
+            for (int pass = 0; pass < NR * (D / 64); ++pass) {
+                const int r = kWide ? pass / (D / 64) : 0, half = pass % (D / 64);
+                // this warp's 8 heads x 64 columns
+                float *dst = sO + (warp * 8 + g) * 64;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int t = half * 8 + j;
+                    const float x = kWide ? acc[t][2 * r] : join(acc[t][0], acc[t][2]);
+                    const float y = kWide ? acc[t][2 * r + 1] : join(acc[t][1], acc[t][3]);
+                    if constexpr (C::ES == 2) {
+                        // columns 8 t + 2 c4, + 1
+                        dst[8 * j + 2 * c4] = x;
+                        dst[8 * j + 2 * c4 + 1] = y;
+                    } else {
+                        // tile 4 i + u holds columns 32 i + 4 n + u, n = 2 c4, 2 c4 + 1
+                        const int i = j >> 2, u = j & 3;
+                        dst[32 * i + 8 * c4 + u] = x;
+                        dst[32 * i + 8 * c4 + 4 + u] = y;
+                    }
+                }
+                __syncthreads();
+                // 4 columns of one head per thread
+                const int hh = threadIdx.x >> 4, col = (threadIdx.x & 15) * 4;
+                const int h = 8 * r + hh;
+                float mx = -INFINITY, z = 0.f;
+                float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sM[(w * 16 + h) * 2]);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float mw = sM[(w * 16 + h) * 2];
+                    const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - mx);
+                    const float lw = sM[(w * 16 + h) * 2 + 1];
+                    // (a warp without a key has l = 0 and o = 0; one whose scores are
+                    // all NaN has m = -inf and l = NaN, which must show)
+                    z += lw == lw ? f * lw : lw;
+                    const float4 x =
+                        *reinterpret_cast<const float4 *>(sO + (w * 8 + hh) * 64 + col);
+                    const float fx = lw == lw ? f : lw;
+                    o[0] += fx * x.x;
+                    o[1] += fx * x.y;
+                    o[2] += fx * x.z;
+                    o[3] += fx * x.w;
+                }
+                if (h < nh) {
+                    if (whole) {
+                        const float inv = z == 0.f ? 0.f : 1.f / z;
+                        T *out = reinterpret_cast<T *>(p.o) + W.e * p.os[0] +
+                                 (h0 + h) * p.os[1] + half * 64 + col;
+                        if constexpr (C::ES == 2)
+                            *reinterpret_cast<uint2 *>(out) = make_uint2(
+                                pk(o[0] * inv, o[1] * inv), pk(o[2] * inv, o[3] * inv));
+                        else
+                            *reinterpret_cast<float4 *>(out) =
+                                make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+                        if (p.lse && half == 0 && (threadIdx.x & 15) == 0)
+                            p.lse[(long long)W.e * p.Hq + h0 + h] =
+                                z == 0.f ? -INFINITY : (mx + log2f(z)) * 0.69314718055994531f;
+                    } else {
+                        float *out = p.part_o + ((long long)part * C::HB + h) * D + half * 64 + col;
+                        *reinterpret_cast<float4 *>(out) = make_float4(o[0], o[1], o[2], o[3]);
+                        if (half == 0 && (threadIdx.x & 15) == 0)
+                            *reinterpret_cast<float2 *>(p.part_ml + ((long long)part * C::HB + h) * 2) =
+                                make_float2(mx, z);
+                    }
+                }
+                __syncthreads();
+            }
+        }
+        W.next(p);
+    }
+    cp_async_wait<0>();
+}
+
+// ------------------------------------------------------------------ join
+// One CTA per segment: nothing to do when one CTA held all its blocks, else the
+// parts of the CTAs that held some, in order.
+template <typename T, int D, int HB>
+__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ DecodeParams p) {
+    __shared__ int scratch[4];
+    const int R = p.Hkv * p.hb;
+    const int e = blockIdx.x / R, r = blockIdx.x % R;
+    int before = 0, after = 0, own = 0;
+    for (int i = threadIdx.x; i < p.n; i += kThreads) {
+        const int x = load_entry(p, i, false).nblk;
+        if (i < e) before += x; else if (i == e) own += x; else after += x;
+    }
+    before = cta_sum(before, scratch);
+    own = cta_sum(own, scratch);
+    after = cta_sum(after, scratch);
+    const long long all = (long long)(before + own + after) * R;
+    const long long s0 = (long long)before * R + (long long)r * own, s1 = s0 + own;
+    // CTA of block x: the largest c with stretch(c) <= x
+    auto owner = [&](long long x) {
+        int c = int(x * p.ctas / all);
+        while (c + 1 < p.ctas && stretch(all, c + 1, p.ctas) <= x) ++c;
+        while (stretch(all, c, p.ctas) > x) --c;
+        return c;
+    };
+    const int c0 = owner(s0), c1 = owner(s1 - 1);
+    wait_previous_kernel();
+    if (c0 == c1) return;
+    const int kvh = r / p.hb, h0 = kvh * p.G + (r % p.hb) * HB;
+    const int nh = min(HB, (kvh + 1) * p.G - h0);
+    for (int i = threadIdx.x; i < nh * (D / 4); i += kThreads) {
+        const int h = i / (D / 4), col = i % (D / 4) * 4;
+        float mx = -INFINITY;
+        for (int c = c0; c <= c1; ++c) {
+            const long long b0 = stretch(all, c, p.ctas);
+            if (b0 == stretch(all, c + 1, p.ctas)) continue;      // no blocks
+            const int part = 2 * c + (b0 < s0 ? 1 : 0);
+            mx = fmaxf(mx, p.part_ml[((long long)part * HB + h) * 2]);
+        }
+        float z = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int c = c0; c <= c1; ++c) {
+            const long long b0 = stretch(all, c, p.ctas);
+            if (b0 == stretch(all, c + 1, p.ctas)) continue;
+            const int part = 2 * c + (b0 < s0 ? 1 : 0);
+            const float2 ml =
+                *reinterpret_cast<const float2 *>(p.part_ml + ((long long)part * HB + h) * 2);
+            const float4 x = *reinterpret_cast<const float4 *>(
+                p.part_o + ((long long)part * HB + h) * D + col);
+            const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
+            const float fx = ml.y == ml.y ? f : ml.y;             // NaN shows
+            z += ml.y == ml.y ? f * ml.y : ml.y;
+            o[0] += fx * x.x;
+            o[1] += fx * x.y;
+            o[2] += fx * x.z;
+            o[3] += fx * x.w;
+        }
+        const float inv = z == 0.f ? 0.f : 1.f / z;
+        T *out = reinterpret_cast<T *>(p.o) + e * p.os[0] + (h0 + h) * p.os[1] + col;
+        if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<uint2 *>(out) =
+                make_uint2(pk(o[0] * inv, o[1] * inv), pk(o[2] * inv, o[3] * inv));
+        else
+            *reinterpret_cast<float4 *>(out) =
+                make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+        if (p.lse && col == 0)
             p.lse[(long long)e * p.Hq + h0 + h] =
                 z == 0.f ? -INFINITY : (mx + log2f(z)) * 0.69314718055994531f;
     }
+}
+
+constexpr int kMaxHeads = 16;   // query heads of a segment, at most
+
+// Query heads of a segment: 9 and more per kv head share a wide one (16-bit pools).
+int segment_heads(int es, int64_t G) { return es == 2 && G > 8 ? 16 : 8; }
+
+int64_t parts_o_bytes(int ctas, int64_t D) { return 2ll * ctas * kMaxHeads * D * 4; }
+int64_t parts_bytes(int ctas, int64_t D) {
+    return parts_o_bytes(ctas, D) + 2ll * ctas * kMaxHeads * 2 * 4;
+}
+
+template <typename T, int D, bool kWide>
+lcx_status launch_decode(DecodeParams &p, cudaStream_t s) {
+    using C = Dec<T, D, kWide>;
+    p.blk = C::BLK;
+    auto kern = paged_decode_kernel<T, D, kWide>;
+    cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess)
+        return fail(LCX_ERR_CUDA, "cudaFuncSetAttribute failed: %s", cudaGetErrorString(e));
+    const long long segments = (long long)p.n * p.Hkv * p.hb;
+    if (segments > 0x7fffffffLL) return fail(LCX_ERR_UNSUPPORTED, "sizes too large");
+    // no more CTAs than blocks there can be
+    const long long most = ((long long)p.MP << p.ps_log2) / p.blk + 1;
+    if (most * p.n > 0x7fffffffLL)
+        return fail(LCX_ERR_UNSUPPORTED, "too many entries for sequences of this length");
+    p.ctas = int(std::min<long long>(p.ctas, segments * most));
+    kern<<<unsigned(p.ctas), kThreads, C::kSmem, s>>>(p);
+    if ((e = cudaGetLastError()) == cudaSuccess && p.ctas > 1)
+        e = launch_dependent(join_kernel<T, D, C::HB>, dim3(unsigned(segments)), dim3(kThreads), 0,
+                             s, p);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return fail(LCX_ERR_CUDA, "paged_decode launch failed: %s", cudaGetErrorString(e));
+    return LCX_OK;
 }
 
 }  // namespace
@@ -155,7 +755,7 @@ extern "C" int64_t lcx_paged_decode_workspace_bytes(int64_t n, int64_t Hq, int64
     if (n < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (D != 64 && D != 128) ||
         n > (int64_t(1) << 20) || Hq > 65536)
         return -1;
-    return 0;
+    return lcx::parts_bytes(2 * lcx::device_sms(), D);
 }
 
 extern "C" lcx_status lcx_paged_decode(const lcx_paged_cache *cache,
@@ -213,13 +813,15 @@ extern "C" lcx_status lcx_paged_decode(const lcx_paged_cache *cache,
     p.Hq = int(g->Hq);
     p.Hkv = c.H;
     p.G = p.Hq / p.Hkv;
-    p.hb = (p.G + kGB - 1) / kGB;
+    const int heads = segment_heads(c.es, p.G);
+    p.hb = (p.G + heads - 1) / heads;
     p.S = c.S;
     p.MP = c.MP;
     p.P = c.P;
     p.ps_log2 = c.ps_log2;
-    p.window = g->window;
-    p.sinks = g->sinks;
+    const int64_t big = int64_t(1) << 30;   // no cache is longer
+    p.window = int(g->window >= big ? 0 : g->window);
+    p.sinks = int(std::min(g->sinks, big));
     p.rotate = (g->flags & LCX_DECODE_PREROTATED) || g->rope.mode == LCX_ROPE_NONE ? 0 : 1;
     p.half = g->rope.pairing == LCX_PAIR_HALF;
     float ms = 1.f;
@@ -227,18 +829,17 @@ extern "C" lcx_status lcx_paged_decode(const lcx_paged_cache *cache,
     const double scale =
         g->softmax_scale > 0.f ? double(g->softmax_scale) : 1.0 / std::sqrt(double(c.D));
     p.c_log2 = float(scale * (p.rotate ? double(ms) : 1.0) * 1.4426950408889634);
-    const long long grid = (long long)p.n * p.Hkv * p.hb;
-    if (grid > 0x7fffffffLL) return fail(LCX_ERR_UNSUPPORTED, "sizes too large");
+    p.ctas = 2 * device_sms();
+    p.part_o = static_cast<float *>(workspace);
+    p.part_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                          parts_o_bytes(p.ctas, c.D));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const unsigned gr = unsigned(grid);
-    if (c.es == 2)
-        c.D == 128 ? paged_decode_kernel<__nv_bfloat16, 128><<<gr, kWarps * 32, 0, s>>>(p)
-                   : paged_decode_kernel<__nv_bfloat16, 64><<<gr, kWarps * 32, 0, s>>>(p);
-    else
-        c.D == 128 ? paged_decode_kernel<float, 128><<<gr, kWarps * 32, 0, s>>>(p)
-                   : paged_decode_kernel<float, 64><<<gr, kWarps * 32, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess)
-        return fail(LCX_ERR_CUDA, "paged_decode launch failed: %s", cudaGetErrorString(e));
-    return LCX_OK;
+    if (c.es == 4)
+        return c.D == 128 ? launch_decode<float, 128, false>(p, s)
+                          : launch_decode<float, 64, false>(p, s);
+    if (heads == 16)
+        return c.D == 128 ? launch_decode<__nv_bfloat16, 128, true>(p, s)
+                          : launch_decode<__nv_bfloat16, 64, true>(p, s);
+    return c.D == 128 ? launch_decode<__nv_bfloat16, 128, false>(p, s)
+                      : launch_decode<__nv_bfloat16, 64, false>(p, s);
 }

@@ -289,8 +289,9 @@ def paged_append(cache, k, v, seq_ids, start, rope: RopeParams, layer: int = 0, 
 
 def paged_decode_workspace_bytes(cache, n, q_heads) -> int:
     """Workspace bytes of ``paged_decode`` for n entries (lcx_paged_decode_workspace_bytes)."""
-    need = int(load().lcx_paged_decode_workspace_bytes(int(n), int(q_heads), cache.kv_heads,
-                                                       cache.head_dim))
+    with _on(cache):
+        need = int(load().lcx_paged_decode_workspace_bytes(int(n), int(q_heads), cache.kv_heads,
+                                                           cache.head_dim))
     if need < 0:
         raise ValueError("paged_decode: sizes out of range (%d entries, %d heads)" % (n, q_heads))
     return need

@@ -175,6 +175,11 @@ def test_decode_hidden_values_are_never_read():
         b = lcx.paged_decode(c, q, ints([0, 1]), rope, window=37, sinks=3)
         assert torch.isnan(b[0, 4:, 5].float()).all()
         assert torch.equal(a[1], b[1]) and torch.equal(a[0, :4], b[0, :4])
+        c.v_pages[0, pg, sl, 1, 5] = float("inf")
+        c.v_pages[0, pg, sl, 1, 6] = -float("inf")
+        b = lcx.paged_decode(c, q, ints([0, 1]), rope, window=37, sinks=3)
+        assert (b[0, 4:, 5] == float("inf")).all() and (b[0, 4:, 6] == -float("inf")).all()
+        assert torch.equal(a[0, 4:, :5], b[0, 4:, :5]) and torch.equal(a[0, 4:, 7:], b[0, 4:, 7:])
         c.k_pages[0, pg, sl, 0, 3] = float("nan")
         b = lcx.paged_decode(c, q, ints([0, 1]), rope, window=37, sinks=3)
         assert torch.isnan(b[0, :4].float()).all()
