@@ -54,12 +54,15 @@ struct Dec {
     static constexpr int RPI = 32 / CPR;          // rows a warp copies per instruction
     static constexpr int NI = KT / RPI;
     static_assert(!kWide || ES == 2, "wide segments: 16-bit pools");
-    // shared memory: rings, q', the warps' outputs (8 heads x 64 columns at a
-    // time), their statistics, the rings' visibility masks
+    // shared memory: rings, q' in two parts and the next segment's q as it comes,
+    // the warps' outputs (8 heads x CW columns at a time), their statistics, the
+    // rings' visibility masks
     static constexpr int kOffQ = kWarps * kStages * 2 * kHalf;
-    static constexpr int kBytesQ = 8192;
-    static constexpr int kOffO = kOffQ + kBytesQ;
-    static constexpr int kOffM = kOffO + kWarps * 8 * 64 * 4;
+    static constexpr int kBytesQ = HB * ROW;      // q, and each part of q'
+    static constexpr int kOffRaw = kOffQ + 2 * kBytesQ;
+    static constexpr int kOffO = kOffRaw + kBytesQ;
+    static constexpr int CW = kBytesQ > 2048 ? 32 : 64;
+    static constexpr int kOffM = kOffO + kWarps * 8 * CW * 4;
     static constexpr int kOffMask = kOffM + kWarps * 16 * 2 * 4;
     static constexpr int kSmem = kOffMask + kWarps * kStages * 4 + 16;
     static_assert(kSmem <= 115712, "two CTAs per SM");
@@ -137,6 +140,13 @@ struct Cursor {
     }
 };
 
+// What the CTA's threads exchange to find their stretch.
+struct Start {
+    int sum[4];
+    int e, off;
+    Entry x;
+};
+
 // 16-byte chunk c of row r of a tile with CPR chunks per row, moved so that the
 // reads below touch every bank once: 16-bit rows by ldmatrix (8 rows, one chunk);
 // fp32 keys by rows r, r + 1 and four chunks, fp32 values by every other row.
@@ -148,13 +158,14 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c, bool value) {
         return (r * CPR + (c ^ (value ? ((r >> 1) & 3) << 1 : (r & 1) << 2))) * 16;
 }
 
-// x in two tf32 parts (an infinite x has no second part).
+// x in two tf32 parts, both cut (not rounded: three cheap instructions instead of
+// two conversions): x - hi is exact, lo keeps its first 11 bits, so hi + lo is
+// within 2^-21 of x.  An infinite x has no second part.
 __device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
-    const float h = round_tf32(x);
-    float l = x - h;
+    hi = __float_as_uint(x) & 0xffffe000u;
+    float l = x - __uint_as_float(hi);
     l = l == l ? l : 0.f;
-    hi = __float_as_uint(h);
-    lo = __float_as_uint(round_tf32(l));
+    lo = __float_as_uint(l) & 0xffffe000u;
 }
 // Two values in two bf16 parts each, packed.
 __device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint32_t &lo) {
@@ -181,54 +192,70 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int R = p.Hkv * p.hb;
     pdl_launch_dependents();   // the join may be scheduled; it waits for this grid
 
-    // This CTA's stretch [b0, b1) of the block list, and where it starts.
-    int *scan = reinterpret_cast<int *>(sO);
+    // This CTA's stretch [b0, b1) of the block list, and the entry that holds b0:
+    // prefix sums over the entries, 128 at a time (up to 128 entries their lengths
+    // are loaded once, which a short call's latency consists of).
+    Start *st = reinterpret_cast<Start *>(sO);
     Cursor L;
-    int nb = 0;
+    int nb;
     {
-        int mine = 0;
-        for (int e = threadIdx.x; e < p.n; e += kThreads)
-            mine += load_entry(p, e, blockIdx.x == 0).nblk;
-        const long long all = (long long)cta_sum(mine, scan) * R;
-        const long long b0 = stretch(all, blockIdx.x, p.ctas);
-        nb = int(stretch(all, blockIdx.x + 1, p.ctas) - b0);
-        if (nb == 0) return;
-        // the entry that holds b0: prefix sums, 128 entries at a time
+        Entry mine;
+        mine.nblk = 0;
+        if (threadIdx.x < p.n) mine = load_entry(p, threadIdx.x, blockIdx.x == 0);
+        int rest = 0;
+        for (int e = threadIdx.x + kThreads; e < p.n; e += kThreads)
+            rest += load_entry(p, e, blockIdx.x == 0).nblk;
+        long long all = 0;
+        if (p.n > kThreads) all = (long long)cta_sum(mine.nblk + rest, st->sum) * R;
         long long before = 0;          // blocks per head block of the entries before
-        int base = 0;
-        for (;; base += kThreads) {
-            const int e = base + threadIdx.x;
-            const int here = e < p.n ? load_entry(p, e, false).nblk : 0;
-            int incl = here;
+        long long b0 = 0;
+        nb = 0;
+        for (int base = 0; base < p.n; base += kThreads) {
+            if (base > 0) {
+                mine.nblk = 0;
+                if (base + threadIdx.x < p.n) mine = load_entry(p, base + threadIdx.x, false);
+            }
+            int incl = mine.nblk;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += y;
             }
             __syncthreads();
-            if (lane == 31) scan[warp] = incl;
-            if (threadIdx.x == 0) scan[4] = -1;
+            if (lane == 31) st->sum[warp] = incl;
+            if (threadIdx.x == 0) st->e = -1;
             __syncthreads();
-            for (int w = 0; w < warp; ++w) incl += scan[w];
-            const long long end = before + incl;
-            if (here > 0 && end * R > b0 && (end - here) * R <= b0) {
-                scan[4] = e;
-                scan[5] = int(b0 - (end - here) * R);
+            const int s0 = st->sum[0], s1 = st->sum[1], s2 = st->sum[2], s3 = st->sum[3];
+            incl += (warp > 0 ? s0 : 0) + (warp > 1 ? s1 : 0) + (warp > 2 ? s2 : 0);
+            const int total = s0 + s1 + s2 + s3;
+            if (base == 0) {
+                if (p.n <= kThreads) all = (long long)total * R;
+                b0 = stretch(all, blockIdx.x, p.ctas);
+                nb = int(stretch(all, blockIdx.x + 1, p.ctas) - b0);
+                if (nb == 0) return;
             }
-            before += scan[0] + scan[1] + scan[2] + scan[3];
+            const long long end = (before + incl) * R, begin = end - (long long)mine.nblk * R;
+            if (begin <= b0 && b0 < end) {
+                st->e = base + threadIdx.x;
+                st->off = int(b0 - begin);
+                st->x = mine;
+            }
+            before += total;
             __syncthreads();
-            if (scan[4] >= 0 || base + kThreads >= p.n) break;
+            if (st->e >= 0) break;
         }
-        L.e = scan[4];
-        const int off = scan[5];
-        __syncthreads();
+        L.e = st->e;
         if (L.e < 0) return;           // not reached: b0 < all
-        L.x = load_entry(p, L.e, false);
-        L.r = off / L.x.nblk;
-        L.blk = off % L.x.nblk;
+        L.x = st->x;
+        L.r = st->off / L.x.nblk;
+        L.blk = st->off % L.x.nblk;
+        __syncthreads();
     }
     Cursor W = L;                      // the tile in use; L the next tile to copy
     int first_blk = W.blk;             // first block of the current segment here
+    int start_b = 0;                   // the iteration it began in
+    int angle_e = -1;                  // the entry cs and sn belong to
+    float cs = 1.f, sn = 0.f;
 
     // Page and slot of this lane's key of the tile at L, loaded one tile early so
     // that the copies do not wait for the table.
@@ -244,6 +271,19 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     int to_copy = nb;
     lookup();
+    // q of segment (e, r), as it is, on the way to shared memory (it joins the
+    // thread's next copy group)
+    auto copy_q = [&](int e, int r) {
+        const int kvh = r / p.hb, h0 = kvh * p.G + (r % p.hb) * C::HB;
+        const int nh = min(C::HB, (kvh + 1) * p.G - h0);
+        const uint32_t dst = smem_u32(sm + C::kOffRaw);
+        for (int i = threadIdx.x; i < C::HB * C::CPR; i += kThreads) {
+            const int h = i / C::CPR, c = i % C::CPR;
+            const char *src = p.q + (e * p.qs[0] + (h0 + h) * p.qs[1]) * C::ES + 16 * c;
+            cp_async16(dst + 16 * i, h < nh ? src : p.q, h < nh ? 16 : 0);
+        }
+    };
+    copy_q(W.e, W.r);
     auto copy_tile = [&](int stage) {
         if (to_copy > 0) {
             const int v = L.blk * C::BLK + warp * C::KT + lane;
@@ -287,25 +327,29 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     int stage = 0;
     for (int b = 0; b < nb; ++b) {
+        // groups of two iterations ago and before have arrived: this tile, and the q
+        // of a segment announced that long ago
+        cp_async_wait<kStages - 2>();
         if (b == 0 || W.blk == 0) {
             // -------------------------------------------------- a segment starts
+            if (b > 0 && b - start_b < 2) cp_async_wait<0>();
+            start_b = b;
             first_blk = W.blk;
-            const int kvh = W.r / p.hb, h0 = kvh * p.G + (W.r % p.hb) * C::HB;
-            const int nh = min(C::HB, (kvh + 1) * p.G - h0);
-            const T *q = reinterpret_cast<const T *>(p.q) + W.e * p.qs[0];
-            // one thread per pair; the heads share its angle
-            for (int pr = threadIdx.x % (D / 2); pr < D / 2; pr += kThreads) {
+            if (W.e != angle_e) {
+                // one pair per thread; the entry's heads share its angle
+                angle_e = W.e;
+                if (p.rotate) rope_sincos(W.x.len - 1, p.theta[threadIdx.x % (D / 2)], &cs, &sn);
+            }
+            __syncthreads();
+            {
                 constexpr int kStep = kThreads / (D / 2);
+                const int pr = threadIdx.x % (D / 2);
                 const int a = p.half ? pr : 2 * pr, b2 = p.half ? pr + D / 2 : 2 * pr + 1;
-                float cs = 1.f, sn = 0.f;
-                if (p.rotate) rope_sincos(W.x.len - 1, p.theta[pr], &cs, &sn);
+                const T *raw = reinterpret_cast<const T *>(sm + C::kOffRaw);
 #pragma unroll 4
                 for (int h = threadIdx.x / (D / 2); h < C::HB; h += kStep) {
-                    float x = 0.f, y = 0.f;
-                    if (h < nh) {
-                        x = static_cast<float>(q[(h0 + h) * p.qs[1] + a]);
-                        y = static_cast<float>(q[(h0 + h) * p.qs[1] + b2]);
-                    }
+                    const float x = static_cast<float>(raw[h * D + a]);
+                    const float y = static_cast<float>(raw[h * D + b2]);
                     const float u = x * cs - y * sn, w = x * sn + y * cs;
                     if constexpr (C::ES == 2) {
                         // rows h (hi) and HB + h (lo), chunks swizzled
@@ -332,6 +376,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
             __syncthreads();
+            if (b + W.x.nblk - W.blk < nb) {       // the stretch goes on behind this segment
+                const bool more = W.r + 1 < R;
+                copy_q(more ? W.e : W.e + 1, more ? W.r + 1 : 0);
+            }
             if constexpr (C::ES == 2 && !kWide) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
@@ -362,7 +410,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
         }
         // ------------------------------------------------------ one tile
-        cp_async_wait<kStages - 2>();
         __syncwarp();
         const uint32_t seen = mask[stage];
         const uint32_t kb = smem_u32(ring + stage * 2 * kHalf), vb = kb + kHalf;
@@ -417,7 +464,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < NS; ++j)
+            for (int j = 0; j < NS; ++j) {
+                // the products with the keys' second parts summed apart: the tensor
+                // core cuts its sums, so short chains lose less
+                float low[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     float4 x;
@@ -430,11 +480,14 @@ __global__ void __launch_bounds__(kThreads, 2)
                     split_tf32(x.y, h[1], w[1]);
                     split_tf32(x.z, h[2], w[2]);
                     split_tf32(x.w, h[3], w[3]);
-                    mma_tf32(s[j], qf[2 * i], w[0], w[1]);
-                    mma_tf32(s[j], qf[2 * i + 1], w[2], w[3]);
+                    mma_tf32(low, qf[2 * i], w[0], w[1]);
+                    mma_tf32(low, qf[2 * i + 1], w[2], w[3]);
                     mma_tf32(s[j], qf[2 * i], h[0], h[1]);
                     mma_tf32(s[j], qf[2 * i + 1], h[2], h[3]);
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[j][i] = join(s[j][i], low[i]);
+            }
         }
         // scores of keys 8 j + 2 c4 + {0, 1}: row g in s[j][0..1], row g + 8 in
         // s[j][2..3] (narrow: the second part of row g)
@@ -535,8 +588,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                         uint32_t h0, w0, h1, w1;
                         split_tf32(x[0][t], h0, w0);
                         split_tf32(x[1][t], h1, w1);
-                        mma_tf32(acc[4 * i + t], a, w0, w1);
-                        mma_tf32(acc[4 * i + t], a, h0, h1);
+                        // (a fresh sum per tile, added in fp32 with rounding)
+                        float o[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma_tf32(o, a, w0, w1);
+                        mma_tf32(o, a, h0, h1);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) acc[4 * i + t][k] += o[k];
                     }
                 }
             }
@@ -566,13 +623,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
 #pragma unroll
-            for (int pass = 0; pass < NR * (D / 64); ++pass) {
-                const int r = kWide ? pass / (D / 64) : 0, half = pass % (D / 64);
-                // this warp's 8 heads x 64 columns
-                float *dst = sO + (warp * 8 + g) * 64;
+            for (int pass = 0; pass < NR * (D / C::CW); ++pass) {
+                const int r = kWide ? pass / (D / C::CW) : 0, part_c = pass % (D / C::CW);
+                // this warp's 8 heads x CW columns
+                float *dst = sO + (warp * 8 + g) * C::CW;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int t = half * 8 + j;
+                for (int j = 0; j < C::CW / 8; ++j) {
+                    const int t = part_c * (C::CW / 8) + j;
                     const float x = kWide ? acc[t][2 * r] : join(acc[t][0], acc[t][2]);
                     const float y = kWide ? acc[t][2 * r + 1] : join(acc[t][1], acc[t][3]);
                     if constexpr (C::ES == 2) {
@@ -587,11 +644,14 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                 }
                 __syncthreads();
-                // 4 columns of one head per thread
-                const int hh = threadIdx.x >> 4, col = (threadIdx.x & 15) * 4;
+                // CW / 16 columns of one head per thread
+                constexpr int CT = C::CW / 16;
+                const int hh = threadIdx.x >> 4, col = (threadIdx.x & 15) * CT;
                 const int h = 8 * r + hh;
                 float mx = -INFINITY, z = 0.f;
-                float o[4] = {0.f, 0.f, 0.f, 0.f};
+                float o[CT];
+#pragma unroll
+                for (int i = 0; i < CT; ++i) o[i] = 0.f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sM[(w * 16 + h) * 2]);
 #pragma unroll
@@ -602,32 +662,35 @@ __global__ void __launch_bounds__(kThreads, 2)
                     // (a warp without a key has l = 0 and o = 0; one whose scores are
                     // all NaN has m = -inf and l = NaN, which must show)
                     z += lw == lw ? f * lw : lw;
-                    const float4 x =
-                        *reinterpret_cast<const float4 *>(sO + (w * 8 + hh) * 64 + col);
                     const float fx = lw == lw ? f : lw;
-                    o[0] += fx * x.x;
-                    o[1] += fx * x.y;
-                    o[2] += fx * x.z;
-                    o[3] += fx * x.w;
+#pragma unroll
+                    for (int i = 0; i < CT; ++i)
+                        o[i] += fx * sO[(w * 8 + hh) * C::CW + col + i];
                 }
                 if (h < nh) {
                     if (whole) {
                         const float inv = z == 0.f ? 0.f : 1.f / z;
                         T *out = reinterpret_cast<T *>(p.o) + W.e * p.os[0] +
-                                 (h0 + h) * p.os[1] + half * 64 + col;
-                        if constexpr (C::ES == 2)
-                            *reinterpret_cast<uint2 *>(out) = make_uint2(
-                                pk(o[0] * inv, o[1] * inv), pk(o[2] * inv, o[3] * inv));
-                        else
-                            *reinterpret_cast<float4 *>(out) =
-                                make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
-                        if (p.lse && half == 0 && (threadIdx.x & 15) == 0)
+                                 (h0 + h) * p.os[1] + part_c * C::CW + col;
+#pragma unroll
+                        for (int i = 0; i < CT; i += 2) {
+                            if constexpr (C::ES == 2)
+                                *reinterpret_cast<uint32_t *>(out + i) =
+                                    pk(o[i] * inv, o[i + 1] * inv);
+                            else
+                                *reinterpret_cast<float2 *>(out + i) =
+                                    make_float2(o[i] * inv, o[i + 1] * inv);
+                        }
+                        if (p.lse && part_c == 0 && (threadIdx.x & 15) == 0)
                             p.lse[(long long)W.e * p.Hq + h0 + h] =
                                 z == 0.f ? -INFINITY : (mx + log2f(z)) * 0.69314718055994531f;
                     } else {
-                        float *out = p.part_o + ((long long)part * C::HB + h) * D + half * 64 + col;
-                        *reinterpret_cast<float4 *>(out) = make_float4(o[0], o[1], o[2], o[3]);
-                        if (half == 0 && (threadIdx.x & 15) == 0)
+                        float *out =
+                            p.part_o + ((long long)part * C::HB + h) * D + part_c * C::CW + col;
+#pragma unroll
+                        for (int i = 0; i < CT; i += 2)
+                            *reinterpret_cast<float2 *>(out + i) = make_float2(o[i], o[i + 1]);
+                        if (part_c == 0 && (threadIdx.x & 15) == 0)
                             *reinterpret_cast<float2 *>(p.part_ml + ((long long)part * C::HB + h) * 2) =
                                 make_float2(mx, z);
                     }
@@ -642,22 +705,35 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // ------------------------------------------------------------------ join
 // One CTA per segment: nothing to do when one CTA held all its blocks, else the
-// parts of the CTAs that held some, in order.
+// parts of the CTAs that held some, in order.  Everything up to the parts' weights
+// is computed by a thread per part; the outputs are then sums of independent loads.
+constexpr int kMaxCtas = 320;       // CTAs of the attention kernel, at most
+
 template <typename T, int D, int HB>
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ DecodeParams p) {
-    __shared__ int scratch[4];
-    const int R = p.Hkv * p.hb;
+    __shared__ int sums[3][kWarps];
+    __shared__ int part[kMaxCtas];
+    __shared__ float weight[HB][kMaxCtas], stat[HB][2];   // stat: maximum, sum
+    const int R = p.Hkv * p.hb, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int e = blockIdx.x / R, r = blockIdx.x % R;
-    int before = 0, after = 0, own = 0;
+    int v[3] = {0, 0, 0};           // blocks of the entries before, of e, behind
     for (int i = threadIdx.x; i < p.n; i += kThreads) {
         const int x = load_entry(p, i, false).nblk;
-        if (i < e) before += x; else if (i == e) own += x; else after += x;
+        v[0] += i < e ? x : 0;
+        v[1] += i == e ? x : 0;
+        v[2] += i > e ? x : 0;
     }
-    before = cta_sum(before, scratch);
-    own = cta_sum(own, scratch);
-    after = cta_sum(after, scratch);
-    const long long all = (long long)(before + own + after) * R;
-    const long long s0 = (long long)before * R + (long long)r * own, s1 = s0 + own;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+        if (lane == 0) sums[k][warp] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 3; ++k) v[k] = sums[k][0] + sums[k][1] + sums[k][2] + sums[k][3];
+    const long long all = (long long)(v[0] + v[1] + v[2]) * R;
+    const long long s0 = (long long)v[0] * R + (long long)r * v[1], s1 = s0 + v[1];
     // CTA of block x: the largest c with stretch(c) <= x
     auto owner = [&](long long x) {
         int c = int(x * p.ctas / all);
@@ -666,48 +742,93 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
         return c;
     };
     const int c0 = owner(s0), c1 = owner(s1 - 1);
-    wait_previous_kernel();
-    if (c0 == c1) return;
     const int kvh = r / p.hb, h0 = kvh * p.G + (r % p.hb) * HB;
     const int nh = min(HB, (kvh + 1) * p.G - h0);
-    for (int i = threadIdx.x; i < nh * (D / 4); i += kThreads) {
-        const int h = i / (D / 4), col = i % (D / 4) * 4;
+    constexpr int PT = (HB * D / 4 + kThreads - 1) / kThreads;   // 4-column pieces per thread
+    float o[PT][4];
+#pragma unroll
+    for (int i = 0; i < PT; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
+    wait_previous_kernel();
+    if (c0 == c1) return;
+    const int cnt = c1 + 1 - c0;
+    for (int k = threadIdx.x; k < kMaxCtas; k += kThreads) {
+        // part of CTA c: its first segment unless its stretch starts before this
+        // one; -1 for a CTA without blocks
+        int x = -1;
+        if (k < cnt) {
+            const int c = c0 + k;
+            const long long b0 = stretch(all, c, p.ctas);
+            if (b0 < stretch(all, c + 1, p.ctas)) x = 2 * c + (b0 < s0 ? 1 : 0);
+        }
+        part[k] = x;
+    }
+    __syncthreads();
+    // weights: a warp per head
+    for (int h = warp; h < nh; h += kWarps) {
+        float2 ml[kMaxCtas / 32];
         float mx = -INFINITY;
-        for (int c = c0; c <= c1; ++c) {
-            const long long b0 = stretch(all, c, p.ctas);
-            if (b0 == stretch(all, c + 1, p.ctas)) continue;      // no blocks
-            const int part = 2 * c + (b0 < s0 ? 1 : 0);
-            mx = fmaxf(mx, p.part_ml[((long long)part * HB + h) * 2]);
+#pragma unroll
+        for (int k = 0; k < kMaxCtas / 32; ++k) {
+            const int x = part[lane + 32 * k];
+            ml[k] = make_float2(-INFINITY, 0.f);
+            if (x >= 0)
+                ml[k] = *reinterpret_cast<const float2 *>(p.part_ml + ((long long)x * HB + h) * 2);
+            mx = fmaxf(mx, ml[k].x);
         }
-        float z = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-            const long long b0 = stretch(all, c, p.ctas);
-            if (b0 == stretch(all, c + 1, p.ctas)) continue;
-            const int part = 2 * c + (b0 < s0 ? 1 : 0);
-            const float2 ml =
-                *reinterpret_cast<const float2 *>(p.part_ml + ((long long)part * HB + h) * 2);
-            const float4 x = *reinterpret_cast<const float4 *>(
-                p.part_o + ((long long)part * HB + h) * D + col);
-            const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
-            const float fx = ml.y == ml.y ? f : ml.y;             // NaN shows
-            z += ml.y == ml.y ? f * ml.y : ml.y;
-            o[0] += fx * x.x;
-            o[1] += fx * x.y;
-            o[2] += fx * x.z;
-            o[3] += fx * x.w;
+#pragma unroll
+        for (int t = 16; t > 0; t >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, t));
+        float z = 0.f;
+#pragma unroll
+        for (int k = 0; k < kMaxCtas / 32; ++k) {
+            const float f = ml[k].x == -INFINITY ? 0.f : ex2_approx(ml[k].x - mx);
+            const bool nan = ml[k].y != ml[k].y;             // NaN shows
+            z += nan ? ml[k].y : f * ml[k].y;
+            weight[h][lane + 32 * k] = nan ? ml[k].y : f;
         }
-        const float inv = z == 0.f ? 0.f : 1.f / z;
+#pragma unroll
+        for (int t = 16; t > 0; t >>= 1) z += __shfl_xor_sync(0xffffffffu, z, t);
+        if (lane == 0) {
+            stat[h][0] = mx;
+            stat[h][1] = z;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+        const int at = threadIdx.x + i * kThreads;
+        const int h = at / (D / 4), col = at % (D / 4) * 4;
+        if (h >= nh) continue;
+#pragma unroll 8
+        for (int k = 0; k < cnt; ++k) {
+            const int x = part[k];
+            if (x < 0) continue;
+            const float f = weight[h][k];
+            const float4 y =
+                *reinterpret_cast<const float4 *>(p.part_o + ((long long)x * HB + h) * D + col);
+            o[i][0] += f * y.x;
+            o[i][1] += f * y.y;
+            o[i][2] += f * y.z;
+            o[i][3] += f * y.w;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+        const int at = threadIdx.x + i * kThreads;
+        const int h = at / (D / 4), col = at % (D / 4) * 4;
+        if (h >= nh) continue;
+        const float z = stat[h][1], inv = z == 0.f ? 0.f : 1.f / z;
         T *out = reinterpret_cast<T *>(p.o) + e * p.os[0] + (h0 + h) * p.os[1] + col;
         if constexpr (sizeof(T) == 2)
             *reinterpret_cast<uint2 *>(out) =
-                make_uint2(pk(o[0] * inv, o[1] * inv), pk(o[2] * inv, o[3] * inv));
+                make_uint2(pk(o[i][0] * inv, o[i][1] * inv), pk(o[i][2] * inv, o[i][3] * inv));
         else
-            *reinterpret_cast<float4 *>(out) =
-                make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+            *reinterpret_cast<float4 *>(out) = make_float4(o[i][0] * inv, o[i][1] * inv,
+                                                           o[i][2] * inv, o[i][3] * inv);
         if (p.lse && col == 0)
             p.lse[(long long)e * p.Hq + h0 + h] =
-                z == 0.f ? -INFINITY : (mx + log2f(z)) * 0.69314718055994531f;
+                z == 0.f ? -INFINITY : (stat[h][0] + log2f(z)) * 0.69314718055994531f;
     }
 }
 
@@ -715,6 +836,9 @@ constexpr int kMaxHeads = 16;   // query heads of a segment, at most
 
 // Query heads of a segment: 9 and more per kv head share a wide one (16-bit pools).
 int segment_heads(int es, int64_t G) { return es == 2 && G > 8 ? 16 : 8; }
+
+// Two CTAs per SM.
+int decode_ctas() { return std::min(2 * device_sms(), kMaxCtas); }
 
 int64_t parts_o_bytes(int ctas, int64_t D) { return 2ll * ctas * kMaxHeads * D * 4; }
 int64_t parts_bytes(int ctas, int64_t D) {
@@ -755,7 +879,7 @@ extern "C" int64_t lcx_paged_decode_workspace_bytes(int64_t n, int64_t Hq, int64
     if (n < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (D != 64 && D != 128) ||
         n > (int64_t(1) << 20) || Hq > 65536)
         return -1;
-    return lcx::parts_bytes(2 * lcx::device_sms(), D);
+    return lcx::parts_bytes(lcx::decode_ctas(), D);
 }
 
 extern "C" lcx_status lcx_paged_decode(const lcx_paged_cache *cache,
@@ -829,7 +953,7 @@ extern "C" lcx_status lcx_paged_decode(const lcx_paged_cache *cache,
     const double scale =
         g->softmax_scale > 0.f ? double(g->softmax_scale) : 1.0 / std::sqrt(double(c.D));
     p.c_log2 = float(scale * (p.rotate ? double(ms) : 1.0) * 1.4426950408889634);
-    p.ctas = 2 * device_sms();
+    p.ctas = decode_ctas();
     p.part_o = static_cast<float *>(workspace);
     p.part_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) +
                                           parts_o_bytes(p.ctas, c.D));

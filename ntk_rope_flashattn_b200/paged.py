@@ -18,7 +18,7 @@ page) skips the entry and is reported through the optional ``status`` tensor
 """
 import ctypes
 
-from . import RopeParams, _check, _dtype_code, _RopeParams, _same_device, _stream, load
+from . import RopeParams, _check, _dtype_code, _RopeParams, _same_device, load
 
 LCX_ERR_NO_PAGES = 5
 LCX_PAGES_MAX_ENTRIES = 1024
@@ -116,6 +116,8 @@ class PagedCache:
         self.free_pages = self.meta[a + b + p:a + b + 2 * p]
         self.n_free = self.meta[a + b + 2 * p:]
         self.scratch = torch.zeros(n_scratch, dtype=torch.int32, device=device)
+        self._struct = ctypes.byref(self._c())     # the buffers never change
+        self._workspace_bytes = {}
         self.reset()
 
     def reset(self):
@@ -148,22 +150,29 @@ def _index(cache, **tensors):
     import torch
     out = []
     for name, t in tensors.items():
-        if t is not None:
-            if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1:
-                raise ValueError("%s must be a 1-D int32 tensor" % name)
-            if not t.is_cuda or t.device != cache.device:
-                raise ValueError("%s must be a CUDA tensor on %s (got %s)" % (name, cache.device,
-                                                                             t.device))
-            if not t.is_contiguous():
-                raise ValueError("%s must be contiguous" % name)
-        out.append(None if t is None else ctypes.c_void_p(t.data_ptr()))
+        if t is None:
+            out.append(None)
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1:
+            raise ValueError("%s must be a 1-D int32 tensor" % name)
+        if t.device != cache.device:
+            raise ValueError("%s must be a CUDA tensor on %s (got %s)" % (name, cache.device,
+                                                                         t.device))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+        out.append(t.data_ptr())
     return out
 
 
-def _on(cache):
-    """The cache's device made current, and its current stream."""
+def _launch(cache, call, *args):
+    """call(*args, stream) with the cache's device current, on its current stream."""
     import torch
-    return torch.cuda.device(cache.device)
+    dev = cache.device.index
+    if torch.cuda.current_device() == dev:
+        _check(call(*args, torch.cuda.current_stream().cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(call(*args, torch.cuda.current_stream().cuda_stream))
 
 
 def pages_extend(cache, seq_ids, n_new=None, start=None, status=None):
@@ -178,9 +187,7 @@ def pages_extend(cache, seq_ids, n_new=None, start=None, status=None):
     elif start.shape != seq_ids.shape:
         raise ValueError("start must have one value per entry")
     ids, nn, st, word = _index(cache, seq_ids=seq_ids, n_new=n_new, start=start, status=status)
-    with _on(cache):
-        _check(load().lcx_pages_extend(ctypes.byref(cache._c()), ids, nn, seq_ids.numel(), st, word,
-                                       _stream(cache.k_pages)))
+    _launch(cache, load().lcx_pages_extend, cache._struct, ids, nn, seq_ids.numel(), st, word)
     return start
 
 
@@ -190,24 +197,19 @@ def pages_fork(cache, src, dst, status=None):
     if src.shape != dst.shape:
         raise ValueError("src and dst must have the same length")
     a, b, word = _index(cache, src=src, dst=dst, status=status)
-    with _on(cache):
-        _check(load().lcx_pages_fork(ctypes.byref(cache._c()), a, b, src.numel(), word,
-                                     _stream(cache.k_pages)))
+    _launch(cache, load().lcx_pages_fork, cache._struct, a, b, src.numel(), word)
 
 
 def pages_free(cache, seq_ids, status=None):
     """The sequences end; pages nobody holds return to the free stack."""
     ids, word = _index(cache, seq_ids=seq_ids, status=status)
-    with _on(cache):
-        _check(load().lcx_pages_free(ctypes.byref(cache._c()), ids, seq_ids.numel(), word,
-                                     _stream(cache.k_pages)))
+    _launch(cache, load().lcx_pages_free, cache._struct, ids, seq_ids.numel(), word)
 
 
 def pages_compact(cache, status=None):
     """Move the used pages to the lowest numbers (lcx_pages_compact)."""
     word, = _index(cache, status=status)
-    with _on(cache):
-        _check(load().lcx_pages_compact(ctypes.byref(cache._c()), word, _stream(cache.k_pages)))
+    _launch(cache, load().lcx_pages_compact, cache._struct, word)
 
 
 def pages_copy(cache, src_pages, dst_pages, status=None):
@@ -215,9 +217,7 @@ def pages_copy(cache, src_pages, dst_pages, status=None):
     if src_pages.shape != dst_pages.shape:
         raise ValueError("src_pages and dst_pages must have the same length")
     a, b, word = _index(cache, src_pages=src_pages, dst_pages=dst_pages, status=status)
-    with _on(cache):
-        _check(load().lcx_pages_copy(ctypes.byref(cache._c()), a, b, src_pages.numel(), word,
-                                     _stream(cache.k_pages)))
+    _launch(cache, load().lcx_pages_copy, cache._struct, a, b, src_pages.numel(), word)
 
 
 def _tokens(t, name, heads, D, dtype):
@@ -228,8 +228,25 @@ def _tokens(t, name, heads, D, dtype):
         raise ValueError("%s must be %s" % (name, dtype))
 
 
+_Strides3 = _I64 * 3
+
+
 def _strides3(t):
-    return (_I64 * 3)(*[int(s) for s in t.stride()])
+    return _Strides3(*t.stride())
+
+
+def _rope_c(rope):
+    """The rope's C struct, kept on it while its fields stay the same (factor
+    tables may change in place: built anew)."""
+    if rope.factors is not None or rope.factors_short is not None:
+        return rope._c()
+    key = (rope.mode, rope.head_dim, rope.base, rope.scale, rope.original_max_pos, rope.alpha,
+           rope.beta, rope.pairing, rope.seq_len)
+    kept = rope.__dict__.get("_kept")
+    if kept is None or kept[0] != key:
+        kept = (key, rope._c())
+        rope.__dict__["_kept"] = kept
+    return kept[1]
 
 
 def paged_append(cache, k, v, seq_ids, start, rope: RopeParams, layer: int = 0, cu_new=None,
@@ -279,21 +296,24 @@ def paged_append(cache, k, v, seq_ids, start, rope: RopeParams, layer: int = 0, 
         a.k_out, a.k_out_strides = k_out.data_ptr(), _strides3(k_out)
     a.seq_ids, a.start, a.cu_new, a.dev_status = ids, st, cu, word
     a.n, a.T, a.layer = seq_ids.numel(), T, int(layer)
-    rope_c = rope._c()
+    rope_c = _rope_c(rope)
     a.rope = rope_c
-    with _on(cache):
-        _check(load().lcx_paged_append(ctypes.byref(cache._c()), ctypes.byref(a),
-                                       _stream(cache.k_pages)))
+    _launch(cache, load().lcx_paged_append, cache._struct, ctypes.byref(a))
     return q_out
 
 
 def paged_decode_workspace_bytes(cache, n, q_heads) -> int:
     """Workspace bytes of ``paged_decode`` for n entries (lcx_paged_decode_workspace_bytes)."""
-    with _on(cache):
-        need = int(load().lcx_paged_decode_workspace_bytes(int(n), int(q_heads), cache.kv_heads,
-                                                           cache.head_dim))
-    if need < 0:
-        raise ValueError("paged_decode: sizes out of range (%d entries, %d heads)" % (n, q_heads))
+    need = cache._workspace_bytes.get((n, q_heads))
+    if need is None:
+        import torch
+        with torch.cuda.device(cache.device):
+            need = int(load().lcx_paged_decode_workspace_bytes(int(n), int(q_heads),
+                                                               cache.kv_heads, cache.head_dim))
+        if need < 0:
+            raise ValueError("paged_decode: sizes out of range (%d entries, %d heads)" %
+                             (n, q_heads))
+        cache._workspace_bytes[(n, q_heads)] = need
     return need
 
 
@@ -324,23 +344,12 @@ def paged_decode(cache, q, seq_ids, rope: RopeParams, layer: int = 0, window: in
     if lse is not None and (lse.shape != (n, Hq) or lse.dtype != torch.float32 or
                             not lse.is_contiguous()):
         raise ValueError("lse must be contiguous fp32 [%d, %d]" % (n, Hq))
-    if Hq % cache.kv_heads == 0:
+    if workspace is None and Hq % cache.kv_heads == 0:
         need = paged_decode_workspace_bytes(cache, n, Hq)
-        if workspace is None:
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-    a = _DecodeArgs()
-    a.q, a.o, a.lse = q.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr()
-    a.seq_ids, a.dev_status = ids, word
-    a.n, a.Hq, a.layer = n, Hq, int(layer)
-    a.q_strides, a.o_strides = _strides3(q), _strides3(o)
-    rope_c = rope._c()
-    a.rope = rope_c
-    a.window, a.sinks, a.softmax_scale = int(window), int(sinks), float(softmax_scale)
-    a.flags = LCX_DECODE_PREROTATED if prerotated else 0
-    with _on(cache):
-        _check(load().lcx_paged_decode(
-            ctypes.byref(cache._c()), ctypes.byref(a),
-            ctypes.c_void_p(workspace.data_ptr() if workspace is not None else None),
-            0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _stream(cache.k_pages)))
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+    a = _DecodeArgs(q.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(), ids, word,
+                    n, Hq, int(layer), _strides3(q), _strides3(o), _rope_c(rope), int(window),
+                    int(sinks), float(softmax_scale), LCX_DECODE_PREROTATED if prerotated else 0)
+    ws, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    _launch(cache, load().lcx_paged_decode, cache._struct, ctypes.byref(a), ws, size)
     return (o, lse) if return_lse else o

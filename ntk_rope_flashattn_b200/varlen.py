@@ -8,7 +8,8 @@ import ctypes
 
 import numpy as np
 
-from . import RopeParams, _check, _dtype_code, _RopeParams, _same_device, _stream, load
+from . import RopeParams, _check, _dtype_code, _RopeParams, _same_device, load
+from .paged import _rope_c, _strides3
 
 LCX_VARLEN_PREROTATED = 1
 
@@ -90,10 +91,6 @@ class VarlenPlan:
         return self.plan[9 + n:9 + n + n + 1]
 
 
-def _strides3(t):
-    return (_I64 * 3)(*[int(s) for s in t.stride()])
-
-
 def attn_varlen(q, k, v, plan: VarlenPlan, rope: RopeParams, causal: bool = True, window: int = 0,
                 sinks: int = 0, softmax_scale: float = 0.0, return_lse: bool = False,
                 prerotated: bool = False, out=None, lse=None, k_rot=None, status=None,
@@ -147,11 +144,11 @@ def attn_varlen(q, k, v, plan: VarlenPlan, rope: RopeParams, causal: bool = True
     a.Tq, a.Tk, a.Hq, a.Hkv, a.D = Tq, Tk, Hq, Hkv, D
     a.q_strides, a.k_strides = _strides3(q), _strides3(k)
     a.v_strides, a.o_strides = _strides3(v), _strides3(o)
-    rope_c = rope._c()
+    rope_c = _rope_c(rope)
     a.rope = rope_c
     a.window, a.sinks, a.softmax_scale = int(window), int(sinks), float(softmax_scale)
     a.flags = LCX_VARLEN_PREROTATED if prerotated else 0
     a.watchdog_ms = int(watchdog_ms)
     with torch.cuda.device(q.device):
-        _check(load().lcx_attn_varlen(ctypes.byref(a), _stream(q)))
+        _check(load().lcx_attn_varlen(ctypes.byref(a), torch.cuda.current_stream().cuda_stream))
     return (o, lse) if return_lse else o

@@ -71,14 +71,13 @@ def plain_decode(q, rows, lens, ids, rope, window=0, sinks=0, scale=None, prerot
 
 def arithmetic(dtype, G, n):
     """(u_s, u_p) of paged_decode for G query heads per kv head and n keys.  fp32
-    sums of D = 128 products and of n weights; operands in two parts of bf16 (or
-    of tf32), or (16-bit pools, G > 8) one bf16 part."""
-    acc, accp = 128 * 2.0 ** -24, n * 2.0 ** -24 + 2.0 ** -20
+    sums of D = 128 products and of n weights, cut instead of rounded by the tensor
+    core (2^-23 a step); operands in two parts of bf16 (2^-16), of tf32 (2^-21 for
+    each factor of a product), weights in one bf16 part for 16-bit pools and G > 8."""
+    acc, accp = 128 * 2.0 ** -23, n * 2.0 ** -23 + 2.0 ** -20
     if dtype == torch.float32:
-        return 3 * 2.0 ** -22 + acc, 3 * 2.0 ** -22 + accp
-    if G <= 8:
-        return 2.0 ** -16 + acc, 2.0 ** -16 + accp
-    return 2.0 ** -8 + acc, 2.0 ** -8 + accp
+        return 2.0 ** -20 + acc, 2.0 ** -20 + accp
+    return 2.0 ** -16 + acc, (2.0 ** -16 if G <= 8 else 2.0 ** -8) + accp
 
 
 def check_decode(o, lse, want, dtype, G, n, label=""):
@@ -210,6 +209,38 @@ def test_decode_bad_numbers_are_hidden_and_reported():
     b, lse = lcx.paged_decode(c, q, ints([0, 1, 2, 1]), rope, status=status, return_lse=True)
     assert int(status) == lcx.LCX_ERR_INVALID_ARG
     assert (b[1] == 0).all() and torch.isinf(lse[1]).all() and torch.equal(b[2], good[2])
+
+
+@pytest.mark.parametrize("n", [129, 300])
+def test_decode_many_entries(n):
+    """More entries than threads, the same sequences named over and over, padded
+    entries among them: every row as in a call of its own."""
+    lens = [70, 1, 0, 333, 16]
+    rope = lcx.RopeParams("plain", 64)
+    c, _ = cache_of(lens, 16, 2, 64, torch.float32)
+    ids = [(7 * i) % 6 - 1 for i in range(n)]
+    q = randn(8, n, 4, 64, dtype=torch.float32)
+    o, lse = lcx.paged_decode(c, q, ints(ids), rope, return_lse=True)
+    for lo in range(0, n, 97):
+        a, b = lcx.paged_decode(c, q[lo:lo + 97], ints(ids[lo:lo + 97]), rope, return_lse=True)
+        # other cuts of the lists: equal up to fp32 rounding of the joined parts
+        assert (o[lo:lo + 97] - a).abs().max() <= 1e-5
+        fin = torch.isfinite(b)
+        assert torch.equal(torch.isfinite(lse[lo:lo + 97]), fin)
+        assert (lse[lo:lo + 97][fin] - b[fin]).abs().max() <= 1e-5
+    pad = torch.tensor([i < 0 or lens[i] == 0 for i in ids], device="cuda")
+    assert (o[pad] == 0).all() and (lse[pad] == -float("inf")).all()
+
+
+def test_decode_one_sequence_over_every_cta():
+    """One long sequence with one kv head: every CTA holds a part of one segment."""
+    lens = [70001]
+    rope = lcx.RopeParams("plain", 64)
+    for dtype in (torch.bfloat16, torch.float32):
+        c, rows = cache_of(lens, 64, 1, 64, dtype)
+        q = randn(2, 1, 3, 64, dtype=dtype)
+        o, lse = lcx.paged_decode(c, q, ints([0]), rope, return_lse=True)
+        check_decode(o, lse, plain_decode(q, rows, lens, [0], rope), dtype, 3, 70001)
 
 
 def test_decode_on_another_stream_with_its_own_workspace():
