@@ -42,6 +42,7 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kStages = 3;      // ring of a warp: one tile in use, two in flight
 constexpr int kHalf = 4096;     // bytes of a tile's keys, and of its values
+constexpr float kLazy = 8.f;    // log2 growth of the maximum that moves the reference
 
 template <typename T, int D, bool kWide>
 struct Dec {
@@ -88,9 +89,21 @@ struct DecodeParams {
     double theta[64];
 };
 
-// The visible keys of an entry: [0, ns) and [lo, len).
+// The visible keys of an entry: [0, ns) and [lo, len), listed so that every tile's
+// keys lie in one page of a tile or more: the first from place 0 to nsp (ns rounded
+// up to kAlign places), the others from the key loa = lo rounded down on; places
+// without a visible key are copied as zeros and masked.
+constexpr int kAlign = 32;
 struct Entry {
     int id, len, ns, lo, nvis, nblk;
+    __device__ __forceinline__ int nsp() const { return (ns + kAlign - 1) & ~(kAlign - 1); }
+    __device__ __forceinline__ int loa() const { return lo & ~(kAlign - 1); }
+    // key at place v, or -1
+    __device__ __forceinline__ int key(int v) const {
+        if (v < nsp()) return v < ns ? v : -1;
+        const int j = loa() + (v - nsp());
+        return j >= lo && j < len ? j : -1;
+    }
 };
 __device__ __forceinline__ Entry load_entry(const DecodeParams &p, int e, bool report) {
     Entry x;
@@ -106,7 +119,7 @@ __device__ __forceinline__ Entry load_entry(const DecodeParams &p, int e, bool r
     if (bad && report) raise_status(p.status, LCX_ERR_INVALID_ARG);
     x.lo = p.window > 0 ? max(0, x.len - p.window) : 0;
     x.ns = min(p.sinks, x.lo);
-    x.nvis = x.len - x.lo + x.ns;
+    x.nvis = x.len - x.loa() + x.nsp();
     x.nblk = max(1, (x.nvis + p.blk - 1) / p.blk);   // an empty entry writes its zeros
     return x;
 }
@@ -156,6 +169,14 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c, bool value) {
         return (r * CPR + (c ^ (r & 7))) * 16;
     else
         return (r * CPR + (c ^ (value ? ((r >> 1) & 3) << 1 : (r & 1) << 2))) * 16;
+}
+
+// chunk_at of the row `rows` further on (a constant): the tile's base and rows
+// are multiples of 128 bytes, so the exclusive-or acts on the offset itself.
+template <typename T, int CPR>
+__device__ __forceinline__ uint32_t row_at(uint32_t at, int rows, bool value) {
+    const int x = sizeof(T) == 2 ? rows & 7 : value ? ((rows >> 1) & 3) << 1 : (rows & 1) << 2;
+    return (at ^ (x << 4)) + rows * CPR * 16;
 }
 
 // x in two tf32 parts, both cut (not rounded: three cheap instructions instead of
@@ -260,15 +281,25 @@ __global__ void __launch_bounds__(kThreads, 2)
     // Page and slot of this lane's key of the tile at L, loaded one tile early so
     // that the copies do not wait for the table.
     int page = -1, slot = 0;
+    bool wanted = false;               // this lane's place holds a visible key
     auto lookup = [&]() {
-        const int v = L.blk * C::BLK + warp * C::KT + lane;
+        const int key = L.x.key(L.blk * C::BLK + warp * C::KT + lane);
         page = -1;
-        if (lane < C::KT && v < L.x.nvis) {
-            const int key = v < L.x.ns ? v : L.x.lo + (v - L.x.ns);
+        wanted = lane < C::KT && key >= 0;
+        if (wanted) {
             page = __ldg(p.table + (long long)L.x.id * p.MP + (key >> p.ps_log2));
             slot = key & ((1 << p.ps_log2) - 1);
         }
     };
+    // pages of a tile or more: all its keys are neighbours in one page, so one page
+    // number and one address serve all rows
+    const bool run = (1 << p.ps_log2) >= C::KT;
+    // This lane's chunk of row lane / CPR: later rows differ by whole rows and an
+    // exclusive-or with a constant (chunk_at).
+    const int my_row = lane / C::CPR, my_chunk = lane % C::CPR;
+    const uint32_t at_k = chunk_at<T, C::CPR>(my_row, my_chunk, false);
+    const uint32_t at_v = chunk_at<T, C::CPR>(my_row, my_chunk, true);
+    const long long step_k = p.ks[1] * (C::ES * C::RPI), step_v = p.vs[1] * (C::ES * C::RPI);
     int to_copy = nb;
     lookup();
     // q of segment (e, r), as it is, on the way to shared memory (it joins the
@@ -286,26 +317,47 @@ __global__ void __launch_bounds__(kThreads, 2)
     copy_q(W.e, W.r);
     auto copy_tile = [&](int stage) {
         if (to_copy > 0) {
-            const int v = L.blk * C::BLK + warp * C::KT + lane;
-            if (lane < C::KT && v < L.x.nvis && (page < 0 || page >= p.P)) {
+            if (wanted && (page < 0 || page >= p.P)) {
                 page = -1;
                 raise_status(p.status, LCX_ERR_INVALID_ARG);
             }
             const uint32_t seen = __ballot_sync(0xffffffffu, page >= 0);
             const int kvh = L.r / p.hb;
             const uint32_t dst = smem_u32(ring + stage * 2 * kHalf);
-            const int c = lane % C::CPR;
+            const char *k0 = p.kp + (kvh * p.ks[2]) * C::ES + 16 * my_chunk;
+            const char *w0 = p.vp + (kvh * p.vs[2]) * C::ES + 16 * my_chunk;
+            if (run) {
+                // the first visible key's page and the slot of row 0
+                const int first = max(__ffs(seen) - 1, 0);
+                const long long a = max(__shfl_sync(0xffffffffu, page, first), 0);
+                const long long sl =
+                    seen ? __shfl_sync(0xffffffffu, slot, first) - first + my_row : my_row;
+                const char *k = k0 + (a * p.ks[0] + sl * p.ks[1]) * C::ES;
+                const char *w = w0 + (a * p.vs[0] + sl * p.vs[1]) * C::ES;
+                const uint32_t rows = seen >> my_row;
 #pragma unroll
-            for (int i = 0; i < C::NI; ++i) {
-                const int r = i * C::RPI + lane / C::CPR;
-                const int pg = __shfl_sync(0xffffffffu, page, r);
-                const int sl = __shfl_sync(0xffffffffu, slot, r);
-                const int bytes = pg >= 0 ? 16 : 0;
-                const long long a = max(pg, 0);
-                const char *k = p.kp + (a * p.ks[0] + sl * p.ks[1] + kvh * p.ks[2]) * C::ES + 16 * c;
-                const char *w = p.vp + (a * p.vs[0] + sl * p.vs[1] + kvh * p.vs[2]) * C::ES + 16 * c;
-                cp_async16(dst + chunk_at<T, C::CPR>(r, c, false), bytes ? k : p.kp, bytes);
-                cp_async16(dst + kHalf + chunk_at<T, C::CPR>(r, c, true), bytes ? w : p.vp, bytes);
+                for (int i = 0; i < C::NI; ++i) {
+                    const int bytes = (rows >> (i * C::RPI)) & 1 ? 16 : 0;
+                    cp_async16(dst + row_at<T, C::CPR>(at_k, i * C::RPI, false), k, bytes);
+                    cp_async16(dst + kHalf + row_at<T, C::CPR>(at_v, i * C::RPI, true), w, bytes);
+                    k += step_k;
+                    w += step_v;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < C::NI; ++i) {
+                    const int r = i * C::RPI + my_row;
+                    const int pg = __shfl_sync(0xffffffffu, page, r);
+                    const int sl = __shfl_sync(0xffffffffu, slot, r);
+                    const int bytes = pg >= 0 ? 16 : 0;
+                    const long long a = max(pg, 0);
+                    const char *k = k0 + (a * p.ks[0] + sl * p.ks[1]) * C::ES;
+                    const char *w = w0 + (a * p.vs[0] + sl * p.vs[1]) * C::ES;
+                    cp_async16(dst + row_at<T, C::CPR>(at_k, i * C::RPI, false),
+                               bytes ? k : p.kp, bytes);
+                    cp_async16(dst + kHalf + row_at<T, C::CPR>(at_v, i * C::RPI, true),
+                               bytes ? w : p.vp, bytes);
+                }
             }
             if (lane == 0) mask[stage] = seen;
             if (--to_copy > 0) {
@@ -319,11 +371,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int s = 0; s < kStages - 1; ++s) copy_tile(s);
 
     constexpr int NT = D / 8;          // output column tiles
+    constexpr uint32_t kAllKeys = C::KT == 32 ? 0xffffffffu : (1u << (C::KT % 32)) - 1;
     constexpr int QF = C::ES == 2 ? (kWide ? 1 : D / 16) : D / 8;
     uint32_t qf[QF][4];                // q' as A fragments (wide: read per tile)
     float acc[NT][4];
     float m[2], l[2];                  // rows g and g + 8 (narrow: row g alone)
     const uint32_t sq = smem_u32(sm + C::kOffQ);
+    // where this lane reads its fragments in a tile (16-bit: ldmatrix rows; fp32:
+    // 16-byte pieces); other places differ by constants
+    const uint32_t rd_k = C::ES == 2 ? chunk_at<T, C::CPR>(lane & 7, lane >> 3, false)
+                                     : chunk_at<T, C::CPR>(g, c4, false);
+    const uint32_t rd_v = C::ES == 2 ? chunk_at<T, C::CPR>(lane & 15, lane >> 4, true)
+                                     : chunk_at<T, C::CPR>(2 * c4, g, true);
 
     int stage = 0;
     for (int b = 0; b < nb; ++b) {
@@ -420,13 +479,13 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[j][i] = 0.f;
         if constexpr (C::ES == 2) {
-            float s2[kWide ? NS : 1][4];
-            if constexpr (kWide) {
+            // second sums: the products with q's second part (wide), or every other
+            // step (shorter chains of dependent products)
+            float s2[NS][4];
 #pragma unroll
-                for (int j = 0; j < NS; ++j)
+            for (int j = 0; j < NS; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s2[j][i] = 0.f;
-            }
+                for (int i = 0; i < 4; ++i) s2[j][i] = 0.f;
 #pragma unroll
             for (int k = 0; k < D / 16; k += 2) {
                 uint32_t a0[4], a1[4], l0[4], l1[4];
@@ -443,8 +502,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int j = 0; j < NS; ++j) {
                     uint32_t kf[4];        // 8 keys x 32 columns
-                    ldmatrix4(kf, kb + chunk_at<T, C::CPR>(8 * j + (lane & 7), 2 * k + (lane >> 3),
-                                                           false));
+                    ldmatrix4(kf, kb + (rd_k ^ ((2 * k & 7) << 4)) + (2 * k >> 3) * 128 +
+                                      j * 8 * C::ROW);
                     if constexpr (kWide) {
                         mma_bf16(s[j], a0, kf[0], kf[1]);
                         mma_bf16(s2[j], l0, kf[0], kf[1]);
@@ -452,28 +511,29 @@ __global__ void __launch_bounds__(kThreads, 2)
                         mma_bf16(s2[j], l1, kf[2], kf[3]);
                     } else {
                         mma_bf16(s[j], qf[k], kf[0], kf[1]);
-                        mma_bf16(s[j], qf[k + 1], kf[2], kf[3]);
+                        mma_bf16(s2[j], qf[k + 1], kf[2], kf[3]);
                     }
                 }
             }
-            if constexpr (kWide) {
 #pragma unroll
-                for (int j = 0; j < NS; ++j)
+            for (int j = 0; j < NS; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s[j][i] = join(s[j][i], s2[j][i]);
-            }
+                for (int i = 0; i < 4; ++i)
+                    s[j][i] = kWide ? join(s[j][i], s2[j][i]) : s[j][i] + s2[j][i];
         } else {
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
                 // the products with the keys' second parts summed apart: the tensor
                 // core cuts its sums, so short chains lose less
-                float low[4] = {0.f, 0.f, 0.f, 0.f};
+                float low[4] = {0.f, 0.f, 0.f, 0.f}, low2[4] = {0.f, 0.f, 0.f, 0.f};
+                float s2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     float4 x;
                     asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
                                  : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                                 : "r"(kb + chunk_at<T, C::CPR>(8 * j + g, 4 * i + c4, false))
+                                 : "r"(kb + (rd_k ^ ((4 * i & 7) << 4)) + (4 * i >> 3) * 128 +
+                                       j * 8 * C::ROW)
                                  : "memory");
                     uint32_t h[4], w[4];
                     split_tf32(x.x, h[0], w[0]);
@@ -481,47 +541,56 @@ __global__ void __launch_bounds__(kThreads, 2)
                     split_tf32(x.z, h[2], w[2]);
                     split_tf32(x.w, h[3], w[3]);
                     mma_tf32(low, qf[2 * i], w[0], w[1]);
-                    mma_tf32(low, qf[2 * i + 1], w[2], w[3]);
+                    mma_tf32(low2, qf[2 * i + 1], w[2], w[3]);
                     mma_tf32(s[j], qf[2 * i], h[0], h[1]);
-                    mma_tf32(s[j], qf[2 * i + 1], h[2], h[3]);
+                    mma_tf32(s2, qf[2 * i + 1], h[2], h[3]);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[j][i] = join(s[j][i], low[i]);
+                for (int i = 0; i < 4; ++i) s[j][i] = join(s[j][i] + s2[i], low[i] + low2[i]);
             }
         }
         // scores of keys 8 j + 2 c4 + {0, 1}: row g in s[j][0..1], row g + 8 in
         // s[j][2..3] (narrow: the second part of row g)
         constexpr int NR = kWide ? 2 : 1;
+        if constexpr (!kWide) {
 #pragma unroll
-        for (int j = 0; j < NS; ++j)
+            for (int j = 0; j < NS; ++j)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const bool in = (seen >> (8 * j + 2 * c4 + i)) & 1;
-                if constexpr (kWide) {
-                    s[j][i] = in ? s[j][i] * p.c_log2 : -INFINITY;
-                    s[j][i + 2] = in ? s[j][i + 2] * p.c_log2 : -INFINITY;
-                } else {
-                    s[j][i] = in ? join(s[j][i], s[j][i + 2]) * p.c_log2 : -INFINITY;
-                }
-            }
-        float mref[NR];
+                for (int i = 0; i < 2; ++i) s[j][i] = join(s[j][i], s[j][i + 2]);
+        }
+        if (seen != kAllKeys) {
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (!((seen >> (8 * j + 2 * c4 + i)) & 1)) {
+                        s[j][i] = -INFINITY;
+                        if constexpr (kWide) s[j][i + 2] = -INFINITY;
+                    }
+        }
+        // The running reference m (log2 units) follows the maximum only when that
+        // has grown by more than 2^8: the result is the same, the weights stay
+        // below 2^8, and the outputs are rescaled a few times per segment instead
+        // of in most tiles (a tile with a new maximum in one of 8 heads).
+        float mx[NR];
+        bool grew = false;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-            float mx = m[r];
+            float x = fmaxf(s[0][2 * r], s[0][2 * r + 1]);
 #pragma unroll
-            for (int j = 0; j < NS; ++j) mx = fmaxf(mx, fmaxf(s[j][2 * r], s[j][2 * r + 1]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            mref[r] = mx;
+            for (int j = 1; j < NS; ++j) x = fmaxf(x, fmaxf(s[j][2 * r], s[j][2 * r + 1]));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            mx[r] = x * p.c_log2;
+            grew |= mx[r] > m[r] + kLazy;
         }
-        bool grew = mref[0] > m[0];
-        if constexpr (kWide) grew |= mref[1] > m[1];
         if (__any_sync(0xffffffffu, grew)) {
             float al[2];
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
-                al[r] = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - mref[r]);
-                m[r] = mref[r];
+                const float to = fmaxf(m[r], mx[r]);
+                al[r] = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - to);
+                m[r] = to;
                 l[r] *= al[r];
             }
             if constexpr (!kWide) al[1] = al[0];
@@ -534,15 +603,15 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
 #pragma unroll
-        for (int r = 0; r < NR; ++r) mref[r] = m[r] == -INFINITY ? 0.f : m[r];
+        for (int r = 0; r < NR; ++r) {
+            const float mref = m[r] == -INFINITY ? 0.f : m[r];
 #pragma unroll
-        for (int j = 0; j < NS; ++j)
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                s[j][2 * r] = ex2_approx(s[j][2 * r] - mref[r]);
-                s[j][2 * r + 1] = ex2_approx(s[j][2 * r + 1] - mref[r]);
+            for (int j = 0; j < NS; ++j) {
+                s[j][2 * r] = ex2_approx(fmaf(s[j][2 * r], p.c_log2, -mref));
+                s[j][2 * r + 1] = ex2_approx(fmaf(s[j][2 * r + 1], p.c_log2, -mref));
                 l[r] += s[j][2 * r] + s[j][2 * r + 1];
             }
+        }
         if constexpr (C::ES == 2) {
 #pragma unroll
             for (int j = 0; j < NS; j += 2) {
@@ -559,8 +628,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int t = 0; t < NT; t += 2) {
                     uint32_t vf[4];        // 16 keys x 16 columns
-                    ldmatrix4_trans(vf, vb + chunk_at<T, C::CPR>(8 * j + (lane & 15),
-                                                                 t + (lane >> 4), true));
+                    ldmatrix4_trans(vf, vb + (rd_v ^ ((t & 7) << 4)) + (t >> 3) * 128 +
+                                            j * 8 * C::ROW);
                     mma_bf16(acc[t], a, vf[0], vf[1]);
                     mma_bf16(acc[t + 1], a, vf[2], vf[3]);
                 }
@@ -580,8 +649,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     for (int k = 0; k < 2; ++k)
                         asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
                                      : "=f"(x[k][0]), "=f"(x[k][1]), "=f"(x[k][2]), "=f"(x[k][3])
-                                     : "r"(vb + chunk_at<T, C::CPR>(8 * j + 2 * c4 + k, 8 * i + g,
-                                                                    true))
+                                     : "r"(vb + rd_v + i * 128 + (8 * j + k) * C::ROW)
                                      : "memory");
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {

@@ -169,10 +169,10 @@ def _launch(cache, call, *args):
     import torch
     dev = cache.device.index
     if torch.cuda.current_device() == dev:
-        _check(call(*args, torch.cuda.current_stream().cuda_stream))
+        _check(call(*args, torch.cuda.current_stream(dev).cuda_stream))
     else:
         with torch.cuda.device(dev):
-            _check(call(*args, torch.cuda.current_stream().cuda_stream))
+            _check(call(*args, torch.cuda.current_stream(dev).cuda_stream))
 
 
 def pages_extend(cache, seq_ids, n_new=None, start=None, status=None):
