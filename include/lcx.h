@@ -562,7 +562,13 @@ LCX_API int64_t lcx_varlen_plan_ints(const int32_t *lens_q, const int32_t *lens_
 LCX_API lcx_status lcx_varlen_plan(const int32_t *lens_q, const int32_t *lens_k, int64_t n,
                                    int32_t *plan, int64_t ints, lcx_varlen_info *info);
 
+/* Workspace bytes of lcx_attn_varlen (-1: arguments out of range).  Host only. */
+LCX_API int64_t lcx_varlen_workspace_bytes(const lcx_varlen_info *info, int64_t Hkv, int64_t D,
+                                           int32_t dtype);
+
 #define LCX_VARLEN_PREROTATED 1u /* q and k are already rotated (mscale included)      */
+#define LCX_VARLEN_TEST_STALL 0x80000000u /* test hook for the watchdog (bf16), as
+                                  LCX_ATTN_TEST_STALL; never set in production       */
 
 typedef struct {
     const void *q;             /* DEVICE [Tq, Hq, D], Tq >= total_q                    */
@@ -570,10 +576,10 @@ typedef struct {
     void *o;                   /* DEVICE [Tq, Hq, D]                                   */
     float *lse;                /* DEVICE [Hq, Tq] contiguous, or NULL                  */
     const int32_t *plan;       /* DEVICE copy of the plan, 16-byte aligned             */
-    void *k_rot;               /* DEVICE scratch [total_k, Hkv, D] of dtype for the
-                                  rotated keys; unused with LCX_VARLEN_PREROTATED or
-                                  rope mode NONE                                      */
-    int64_t k_rot_bytes;
+    void *workspace;           /* DEVICE, 256-byte aligned, for the rotated keys; not
+                                  shared by calls in flight; unused with
+                                  LCX_VARLEN_PREROTATED or rope mode NONE             */
+    int64_t workspace_bytes;   /* lcx_varlen_workspace_bytes                          */
     int32_t *dev_status;       /* as lcx_attn_args                                     */
     lcx_varlen_info info;      /* the plan's info                                      */
     int32_t dtype, causal;
@@ -596,8 +602,14 @@ typedef struct {
  * keys) gets o = 0, lse = -inf.  Rows of o and lse at total_q and beyond are
  * left as they were.  NaN or infinity in a key or value that a query does not
  * see leaves that query alone.
- *   Supported: D 64 or 128, full rotary; bf16 (tensor cores; q', k' and the
- *   weights rounded to bf16, fp32 accumulation) or fp32 (fp32 arithmetic).
+ *   Supported: D 64 or 128, full rotary.
+ *   Arithmetic: bf16: tensor-core products with fp32 accumulation; q' and k'
+ *   rounded to fp16 (rows out of its range scaled by a power of two), in two fp16
+ *   parts for row blocks that start before position 127 or see fewer keys; given
+ *   rotated inputs enter as they are; the weights rounded to bf16, their sum not.
+ *   fp32: fp32 products.
+ *   dev_status: LCX_ERR_TIMEOUT after an expired wait, as lcx_attn_fwd (o and lse
+ *   are then undefined); LCX_ERR_INVALID_ARG for a plan that is not info's.
  */
 LCX_API lcx_status lcx_attn_varlen(const lcx_varlen_args *args, void *stream);
 

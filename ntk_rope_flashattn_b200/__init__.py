@@ -37,7 +37,7 @@ EXPORTED = ("lcx_rope_table", "lcx_apply_rope", "lcx_attn_fwd", "lcx_attn_fwd_sp
             "lcx_paged_scratch_ints", "lcx_pages_extend", "lcx_pages_fork", "lcx_pages_free",
             "lcx_pages_compact", "lcx_pages_copy", "lcx_paged_append", "lcx_paged_decode",
             "lcx_paged_decode_workspace_bytes", "lcx_varlen_plan_ints", "lcx_varlen_plan",
-            "lcx_attn_varlen")
+            "lcx_varlen_workspace_bytes", "lcx_attn_varlen")
 
 
 class LcxError(RuntimeError):
@@ -551,4 +551,4 @@ from . import paged, varlen                                              # noqa:
 from .paged import (LCX_ERR_NO_PAGES, LCX_PAGES_MAX_ENTRIES, PagedCache,  # noqa: E402,F401
                     paged_append, paged_decode, paged_decode_workspace_bytes, pages_compact,
                     pages_copy, pages_extend, pages_fork, pages_free)
-from .varlen import VarlenPlan, attn_varlen                              # noqa: E402,F401
+from .varlen import VarlenPlan, attn_varlen, varlen_workspace_bytes                              # noqa: E402,F401

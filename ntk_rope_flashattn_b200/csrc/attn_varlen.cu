@@ -3,16 +3,46 @@
 //
 // o_i = sum_j softmax_j(c <q'_i, k'_j>) v_j over the visible keys j of the same
 // sequence ("Long Context: RoPE / YaRN / NTK / MLA", 2.4, 10.1, 10.2), with a
-// running maximum and sum ("8.3 长上下文技术", 8.3.4).  Keys are rotated once per
-// call into scratch, queries as their tile is loaded.
+// running maximum and sum ("8.3 长上下文技术", 8.3.4).
+//
+// bf16: the tcgen05 kernel below; fp32: a kernel of fp32 products behind it.
+//
+// The tcgen05 kernel is bound by the tensor core (4 D flops per visible pair and
+// query head) and, per key tile, by the softmax's 128 x 128 exponentials per query
+// tile.  One CTA per (row block of the plan, pair of query heads), 16 warps:
+//   warps 0-3, 4-7  softmax of query tile 0, 1: one thread per row
+//   warps 8-11      helpers: rotate the query tiles; clean the value tiles at a border
+//   warp 12 / 14    TMA producers of Q and K / of V;  warp 13  MMA issuer
+// Both tiles multiply the same key tiles, so a K/V tile is loaded once for 256
+// query rows, and one tile's softmax overlaps the other's products (order PV0(j),
+// S0(j + 1), PV1(j), S1(j + 1)).  With an odd group the two tiles are consecutive
+// row blocks of one head.
+//
+// Operands of QK^T.  Rotated values are not bf16 numbers, and a logit's rounding
+// error reaches lse unweakened when a row sees few keys.  q' and k' are therefore
+// fp16 (11 bits instead of 8, the same tensor-core rate), each row scaled by a power
+// of two when its largest value leaves fp16's comfortable range (rows scale c; scaled
+// keys, rare, take a slower path), and row blocks that start before position 127, or
+// see fewer keys, add the products with the operands' fp16 remainders ("precise":
+// their few key tiles cost three products instead of one).  Given rotated inputs
+// are bf16 already and enter as they are.
+//
+// Values at a border.  P is zero where a key is hidden, but zero times an infinite or
+// NaN value is NaN, and a tile's last rows may belong to the next sequence.  For the
+// tiles that some row does not see completely the helpers clear rows behind the
+// sequence and non-finite values before the product, and the rows that do see such a
+// value add it at the end.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <new>
 #include <vector>
 
+#include <cuda.h>
+
 #include "paged.cuh"
 #include "rope_angle.cuh"
+#include "sm100.cuh"
 #include "varlen.cuh"
 #include "vec16.cuh"
 
@@ -212,6 +242,955 @@ lcx_status launch_simt(const VarlenParams &p, cudaStream_t s) {
     return LCX_OK;
 }
 
+// ------------------------------------------------------------------ key rotation
+// The rotated keys as the tcgen05 kernel reads them: fp16 parts hi [T][Hkv][D],
+// remainders lo alike (rows before kLoRows, all of them with kAllLo), one scale per
+// row (k' = scale (hi + lo)), and per CTA whether any scale is not 1.
+constexpr int kLoRows = 384;   // a precise block's keys: positions below 127 + 256
+
+struct KeyParams {
+    const __nv_bfloat16 *k;
+    long long st, sh;              // element strides: token, head
+    __half *hi, *lo;
+    float *scale;
+    int *flags;
+    const int *cu;                 // first row of each sequence, n + 1
+    int n, T, H, all_lo;
+    float ms;
+    double theta[64];
+};
+
+// Power of two near 1 / amax when amax leaves [2^-6, 2^14), else 1; *undo its
+// reciprocal.  (bf16 values reach 2^128: the exponent is kept below 126.)
+__device__ __forceinline__ float range_scale(float amax, float *undo) {
+    *undo = 1.f;
+    if ((amax >= 0.015625f && amax < 16384.f) || amax == 0.f || !(amax < INFINITY)) return 1.f;
+    const int e = min(max(int(__float_as_uint(amax) >> 23) - 127, -125), 125);
+    *undo = __uint_as_float(uint32_t(127 + e) << 23);
+    return __uint_as_float(uint32_t(127 - e) << 23);
+}
+
+// 8 values as fp16 parts and (when wanted) remainders.
+__device__ __forceinline__ uint4 half_parts(const float (&y)[8], bool want_lo, uint4 *lo) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        h[e] = pack_f16x2(y[2 * e], y[2 * e + 1]);
+        const float2 f = f16x2_to_f32x2(h[e]);
+        float a = y[2 * e] - f.x, b = y[2 * e + 1] - f.y;
+        a = a == a ? a : 0.f;                 // an infinite value has no remainder
+        b = b == b ? b : 0.f;
+        l[e] = want_lo ? pack_f16x2(a, b) : 0u;
+    }
+    *lo = make_uint4(l[0], l[1], l[2], l[3]);
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+__device__ __forceinline__ float abs_max8(const float (&x)[8]) {
+    const float a = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+    const float b = fmaxf(fmaxf(fabsf(x[4]), fabsf(x[5])), fmaxf(fabsf(x[6]), fabsf(x[7])));
+    return fmaxf(a, b);
+}
+
+// Rotate the pairs of one job: HALF pairs x1[e], x2[e] with angle e; else adjacent
+// pairs of x1 with angle e (x2 unused).
+template <bool kHalf>
+__device__ __forceinline__ void turn(float (&x1)[8], float (&x2)[8], const float *c,
+                                     const float *s) {
+    if constexpr (kHalf) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            const float2 a = make_float2(x1[e], x1[e + 1]), b = make_float2(x2[e], x2[e + 1]);
+            const float2 cc = make_float2(c[e], c[e + 1]), ss = make_float2(s[e], s[e + 1]);
+            const float2 y1 = fma2(b, make_float2(-ss.x, -ss.y), mul2(a, cc));
+            const float2 y2 = fma2(a, ss, mul2(b, cc));
+            x1[e] = y1.x; x1[e + 1] = y1.y;
+            x2[e] = y2.x; x2[e + 1] = y2.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float a = x1[2 * e], b = x1[2 * e + 1];
+            x1[2 * e] = fmaf(-b, s[e], a * c[e]);
+            x1[2 * e + 1] = fmaf(b, c[e], a * s[e]);
+        }
+    }
+}
+
+constexpr int kKeyThreads = 256;
+
+template <int D, bool kHalf>
+struct Job {
+    static constexpr int CPR = kHalf ? D / 16 : D / 8;   // jobs (lanes) per row
+    static constexpr int PPJ = kHalf ? 8 : 4;            // pairs per job
+};
+
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kKeyThreads)
+    varlen_keys_kernel(const __grid_constant__ KeyParams p) {
+    using J = Job<D, kHalf>;
+    constexpr int RPC = kKeyThreads / J::CPR;            // tokens per CTA
+    __shared__ int pos_of[RPC];
+    __shared__ int scaled;
+    pdl_launch_dependents();
+    const int t0 = blockIdx.x * RPC;
+    if (threadIdx.x == 0) scaled = 0;
+    if (threadIdx.x < RPC) {
+        const int t = t0 + threadIdx.x;
+        int lo = 0, hi = p.n;                            // cu[lo] <= t < cu[hi]
+        if (t < p.T) {
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (p.cu[mid] <= t) lo = mid; else hi = mid;
+            }
+            pos_of[threadIdx.x] = t - p.cu[lo];
+        }
+    }
+    __syncthreads();
+    const int q = threadIdx.x % J::CPR, row = threadIdx.x / J::CPR, t = t0 + row;
+    const bool in = t < p.T;                             // whole lane groups agree
+    const int pos = in ? pos_of[row] : 0;
+    float c[J::PPJ], s[J::PPJ];
+#pragma unroll
+    for (int e = 0; e < J::PPJ; ++e) {
+        rope_sincos(pos, p.theta[q * J::PPJ + e], &c[e], &s[e]);
+        c[e] *= p.ms;
+        s[e] *= p.ms;
+    }
+    const int e1 = q * 8, e2 = e1 + D / 2;
+    const bool want_lo = p.all_lo || pos < kLoRows;
+    bool any = false;
+    constexpr int kHB = 4;
+    for (int b = 0; b < p.H; b += kHB) {
+        uint4 va[kHB], vb[kHB];
+#pragma unroll
+        for (int u = 0; u < kHB; ++u) {
+            va[u] = vb[u] = make_uint4(0, 0, 0, 0);
+            if (in && b + u < p.H) {
+                const __nv_bfloat16 *src = p.k + t * p.st + (b + u) * p.sh;
+                va[u] = __ldcs(reinterpret_cast<const uint4 *>(src + e1));
+                if (kHalf) vb[u] = __ldcs(reinterpret_cast<const uint4 *>(src + e2));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kHB; ++u) {
+            float x1[8], x2[8];
+            unpack(va[u], x1);
+            unpack(vb[u], x2);
+            turn<kHalf>(x1, x2, c, s);
+            float mx = kHalf ? fmaxf(abs_max8(x1), abs_max8(x2)) : abs_max8(x1);
+#pragma unroll
+            for (int o = 1; o < J::CPR; o <<= 1)
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            float undo;
+            const float f = range_scale(mx, &undo);
+            if (undo != 1.f) {
+                any = true;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x1[e] *= f;
+                    x2[e] *= f;
+                }
+            }
+            if (!in || b + u >= p.H) continue;
+            const long long at = ((long long)t * p.H + b + u) * D;
+            uint4 lo;
+            *reinterpret_cast<uint4 *>(p.hi + at + e1) = half_parts(x1, want_lo, &lo);
+            if (want_lo) *reinterpret_cast<uint4 *>(p.lo + at + e1) = lo;
+            if (kHalf) {
+                *reinterpret_cast<uint4 *>(p.hi + at + e2) = half_parts(x2, want_lo, &lo);
+                if (want_lo) *reinterpret_cast<uint4 *>(p.lo + at + e2) = lo;
+            }
+            if (q == 0) p.scale[(long long)t * p.H + b + u] = undo;
+        }
+    }
+    if (any) scaled = 1;
+    __syncthreads();
+    if (threadIdx.x == 0) p.flags[blockIdx.x] = scaled;
+}
+
+// ------------------------------------------------------------------ tcgen05 kernel
+constexpr int kThreads = 512, kBM = 128, kBN = 128;
+// registers a thread after the warpgroups re-balance: 176 + 176 + 96 + 64 = 4 x 128
+constexpr int kRegsSoftmax = 176, kRegsHelp = 96, kRegsIssue = 64;
+static_assert(2 * kRegsSoftmax + kRegsHelp + kRegsIssue == 4 * 128, "register file split");
+constexpr int kWarpHelp = 8, kWarpTma = 12, kWarpMma = 13, kWarpTmaV = 14;
+constexpr float kLazy = 15.f;       // log2 growth of a row's maximum that rescales O
+constexpr int kMaxBorder = 8;       // border tiles whose non-finite rows are listed
+
+enum Mode { kTwoHeads = 0, kTwoBlocks = 1, kOneTile = 2 };
+
+struct TcParams {
+    VarlenParams v;
+    const float *k_scale;           // [Tk][Hkv], or NULL: no key is scaled
+    const int *k_flags;             // per CTA of the key rotation
+    int flag_rows;                  // tokens of such a CTA
+    int mode, fp16;                 // fp16: rotated operands; 0: bf16 inputs as they are
+    int head_units;                 // CTAs per row block
+    int stall;                      // the producers issue nothing (watchdog test hook)
+};
+
+template <int D>
+struct Tc {
+    static constexpr int kTile = 128 * D * 2;            // a Q, K or V tile
+    static constexpr int kBox = 128 * 128;               // its 64-column boxes
+    static constexpr int NS = D == 64 ? 4 : 2;           // K stages, and V stages
+    static constexpr int kOffK = 2 * kTile;
+    static constexpr int kOffV = kOffK + NS * kTile;
+    // precise blocks: keys' parts in K stages 0 and 1, values in V stage 0, the query
+    // tiles' remainders in V stage 1 and the next 32 KB
+    static constexpr int kOffQLo = kOffV + kTile;
+    static constexpr int kOffBar = kOffV + NS * kTile + (D == 64 ? 0 : kTile);
+    static constexpr int kSmem = kOffBar + 2048 + 1024;  // barriers; alignment slack
+    static_assert(kSmem <= 232448, "shared memory budget");
+    static constexpr int kColO = 2 * kBN;                // TMEM: S_0, S_1, O_0, O_1
+    static_assert(kColO + 2 * D <= 512, "TMEM budget");
+};
+
+template <int NS>
+struct Bars {
+    uint64_t full_q, ready_q, full_k[NS], empty_k[NS], full_v[NS], full_b[NS], clean_v[NS], empty_v[NS];
+    uint64_t s_ready[2], p_ready[2], o_ready[2], helped, drain;
+    uint32_t tmem_base;
+    int abort, k_scaled, n_border, any_bad;
+    int border_tile[kMaxBorder];
+    uint32_t bad[kMaxBorder][4];    // rows of a border tile with non-finite values
+    float q_scale[2 * kBM];
+};
+
+// A CTA's work: the row block, its two tiles and the key tiles it visits.
+struct Block {
+    VarlenUnit u;
+    int g, h0, nt, hstep, rstep;    // tile t: head h0 + t hstep, rows from t rstep on
+    int ns, jlo, n;                 // key tiles: sink tiles [0, ns), then from jlo on
+    bool precise;
+    __device__ __forceinline__ int tile(int j) const { return j < ns ? j : jlo + (j - ns); }
+    __device__ __forceinline__ int pos(int t) const { return u.pos0 + t * rstep; }
+    __device__ __forceinline__ int rows(int t) const { return min(kBM, u.rows - t * rstep); }
+};
+
+__device__ __forceinline__ Block load_block(const TcParams &p) {
+    Block b;
+    const VarlenParams &v = p.v;
+    const int hu = int(blockIdx.x) % p.head_units;
+    b.u = load_unit(v, int(blockIdx.x) / p.head_units);
+    b.hstep = b.rstep = 0;
+    b.nt = 1;
+    if (p.mode == kTwoHeads) {
+        b.h0 = 2 * hu;
+        b.nt = 2;
+        b.hstep = 1;
+    } else {
+        b.h0 = hu;
+        if (p.mode == kTwoBlocks) {
+            b.rstep = kBM;
+            b.nt = b.u.rows > kBM ? 2 : 1;
+        }
+    }
+    b.g = b.h0 / v.G;
+    const int pa = b.u.pos0, pb = b.u.pos0 + b.u.rows - 1, nk = b.u.nk;
+    const int last = v.causal ? min(pb, nk - 1) : nk - 1;     // last visible key
+    b.jlo = 0;
+    b.ns = 0;
+    if (v.window > 0) {
+        b.jlo = max(0, pa - v.window + 1) / kBN;
+        b.ns = min((v.sinks + kBN - 1) / kBN, b.jlo);
+    }
+    b.n = last < 0 ? 0 : b.ns + (last / kBN - b.jlo + 1);
+    b.precise = p.fp16 && ((v.causal && pa < 127) || (v.window > 0 && v.window < 128) || nk < 128);
+    return b;
+}
+
+// Every row of tile t sees every key of key tile jt.
+__device__ __forceinline__ bool tile_full(const VarlenParams &v, const Block &b, int t, int jt) {
+    const int j0 = jt * kBN, j1 = j0 + kBN - 1;
+    const int i0 = b.pos(t), i1 = i0 + kBM - 1;
+    if (j1 > b.u.nk - 1) return false;
+    if (!v.causal) return true;
+    if (j1 > i0) return false;
+    return v.window <= 0 || j0 >= i1 - v.window + 1 || j1 < v.sinks;
+}
+__device__ __forceinline__ bool is_border(const VarlenParams &v, const Block &b, int jt) {
+    for (int t = 0; t < b.nt; ++t)
+        if (!tile_full(v, b, t, jt)) return true;
+    return false;
+}
+
+// 16-byte chunk fc (8 columns) of row r in a tile of 128-byte swizzled boxes.
+__device__ __forceinline__ uint32_t chunk_off(int r, int fc) {
+    return (fc >> 3) * (128 * 128) + r * 128 + (((fc & 7) ^ (r & 7)) << 4);
+}
+
+// Max of 128 values, four chains of 3-input maxima.
+__device__ __forceinline__ float row_max(const float (&v)[128]) {
+    float m0 = v[0], m1 = v[1], m2 = v[2], m3 = v[3];
+#pragma unroll
+    for (int e = 4; e + 8 <= 124; e += 8) {
+        m0 = max3(m0, v[e], v[e + 1]);
+        m1 = max3(m1, v[e + 2], v[e + 3]);
+        m2 = max3(m2, v[e + 4], v[e + 5]);
+        m3 = max3(m3, v[e + 6], v[e + 7]);
+    }
+    m0 = max3(m0, v[124], v[125]);
+    m1 = max3(m1, v[126], v[127]);
+    return fmaxf(max3(m0, m1, m2), m3);
+}
+
+// The query tiles rotated in shared memory: bf16 -> fp16 parts (and, precise,
+// remainders), one scale per row.  The helper thread handles pairs of one job and
+// rows r0 + RP k, and steps its angles by RP positions (at most 16 steps: 2^-19).
+template <int D, bool kHalf>
+__device__ __forceinline__ void rotate_queries(const TcParams &p, const Block &b, int tw,
+                                               uint8_t *smem, Bars<Tc<D>::NS> &bar,
+                                               volatile int *abort, uint64_t tmo, bool &ok) {
+    using J = Job<D, kHalf>;
+    constexpr int RP = 128 / J::CPR;
+    const int q = tw % J::CPR, r0 = tw / J::CPR;
+    float c[J::PPJ], s[J::PPJ], sc[J::PPJ], ss[J::PPJ];
+    for (int t = 0; t < b.nt; ++t) {
+        // two heads: the same rows, so the same angles; turn both tiles together
+        if (t == 1 && b.rstep == 0) break;
+        const int both = b.rstep == 0 ? b.nt : 1;
+#pragma unroll
+        for (int e = 0; e < J::PPJ; ++e) {
+            const double th = p.v.theta[q * J::PPJ + e];
+            __sincosf(rope_reduced_angle((long long)b.pos(t) + r0, th), &s[e], &c[e]);
+            __sincosf(rope_reduced_angle((long long)RP, th), &ss[e], &sc[e]);
+        }
+        if (t == 0) ok = __all_sync(0xffffffffu, mbar_wait(&bar.full_q, 0, abort, tmo));
+        if (!ok) return;
+#pragma unroll 1
+        for (int k = 0; k < 128 / RP; ++k) {
+            const int r = r0 + k * RP;
+            for (int x = 0; x < both; ++x) {
+                uint8_t *tile = smem + (t + x) * Tc<D>::kTile;
+                const uint32_t oa = chunk_off(r, q), ob = chunk_off(r, q + D / 16);
+                float x1[8], x2[8];
+                unpack(*reinterpret_cast<const uint4 *>(tile + oa), x1);
+                if constexpr (kHalf) unpack(*reinterpret_cast<const uint4 *>(tile + ob), x2);
+                turn<kHalf>(x1, x2, c, s);
+                float mx = kHalf ? fmaxf(abs_max8(x1), abs_max8(x2)) : abs_max8(x1);
+#pragma unroll
+                for (int o = 1; o < J::CPR; o <<= 1)
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                float undo;
+                const float f = range_scale(mx, &undo);
+                if (undo != 1.f) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        x1[e] *= f;
+                        if constexpr (kHalf) x2[e] *= f;
+                    }
+                }
+                if (q == 0) bar.q_scale[(t + x) * kBM + r] = undo;
+                uint8_t *low = smem + Tc<D>::kOffQLo + (t + x) * Tc<D>::kTile;
+                uint4 lo;
+                *reinterpret_cast<uint4 *>(tile + oa) = half_parts(x1, b.precise, &lo);
+                if (b.precise) *reinterpret_cast<uint4 *>(low + oa) = lo;
+                if constexpr (kHalf) {
+                    *reinterpret_cast<uint4 *>(tile + ob) = half_parts(x2, b.precise, &lo);
+                    if (b.precise) *reinterpret_cast<uint4 *>(low + ob) = lo;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < J::PPJ; ++e) {
+                const float nc = fmaf(c[e], sc[e], -s[e] * ss[e]);
+                s[e] = fmaf(c[e], ss[e], s[e] * sc[e]);
+                c[e] = nc;
+            }
+        }
+    }
+}
+
+// Whether any key of the block's sequence is scaled.
+__device__ __forceinline__ bool keys_scaled(const TcParams &p, const Block &b, int tw) {
+    if (!p.k_scale || b.u.nk == 0) return false;
+    const int f0 = b.u.k0 / p.flag_rows, f1 = (b.u.k0 + b.u.nk - 1) / p.flag_rows;
+    bool any = false;
+    for (int f = f0 + tw; f <= f1; f += 128) any |= p.k_flags[f] != 0;
+    return any;
+}
+
+// Helper thread tw cleans row tw of a border tile's values: a row behind the
+// sequence becomes zero, non-finite values become zero and their row is listed.
+template <int D>
+__device__ __forceinline__ void clean_values(uint8_t *tile, int tw, bool behind, uint32_t *bad,
+                                             int *any_bad) {
+    uint32_t hit = 0;
+    if (behind) {
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+            *reinterpret_cast<uint4 *>(tile + chunk_off(tw, c)) = make_uint4(0, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(tile + chunk_off(tw, c));
+            // an exponent of all ones carries into the sign's place
+            hit |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
+                   ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
+        }
+        hit &= 0x80008000u;
+        if (hit) {
+            *any_bad = 1;
+            for (int c = 0; c < D / 8; ++c) {
+                uint32_t *w = reinterpret_cast<uint32_t *>(tile + chunk_off(tw, c));
+                for (int e = 0; e < 4; ++e) {
+                    if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
+                    if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0x0000ffffu;
+                }
+            }
+        }
+    }
+    const uint32_t rows = __ballot_sync(0xffffffffu, hit != 0);
+    if (bad && (tw & 31) == 0) bad[tw >> 5] = rows;
+}
+
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kThreads, 1)
+    varlen_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                  const __grid_constant__ CUtensorMap tml, const __grid_constant__ CUtensorMap tmv,
+                  const __grid_constant__ TcParams p) {
+    using C = Tc<D>;
+    constexpr int NS = C::NS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sK = smem + C::kOffK, *sV = smem + C::kOffV;
+    static_assert(sizeof(Bars<NS>) <= 2048, "barrier block");
+    Bars<NS> &bar = *reinterpret_cast<Bars<NS> *>(smem + C::kOffBar);
+    const VarlenParams &v = p.v;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int *abort = &bar.abort;
+    const uint64_t tmo = v.timeout_ns;
+    const Block B = load_block(p);
+    // K and V stages in use: precise blocks keep the keys' parts in two K stages
+    const int mask = B.precise ? 0 : NS - 1, shift = B.precise ? 0 : (NS == 4 ? 2 : 1);
+
+    if (threadIdx.x == 0) {
+        mbar_init(&bar.full_q, 1);
+        mbar_init(&bar.ready_q, 128);
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&bar.full_k[s], 1);
+            mbar_init(&bar.empty_k[s], 1);
+            mbar_init(&bar.full_v[s], 1);
+            mbar_init(&bar.full_b[s], 1);
+            mbar_init(&bar.clean_v[s], 128);
+            mbar_init(&bar.empty_v[s], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&bar.s_ready[t], 1);
+            mbar_init(&bar.p_ready[t], 128);
+            mbar_init(&bar.o_ready[t], 1);
+        }
+        mbar_init(&bar.helped, 128);
+        mbar_init(&bar.drain, 1);
+        bar.abort = 0;
+        bar.k_scaled = 0;
+        bar.n_border = 0;
+        bar.any_bad = 0;
+        fence_mbar_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(&bar.tmem_base, 512);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar.tmem_base;
+    bool pre = false;   // thread 0: an earlier CTA's wait ran out already
+    if (threadIdx.x == 0 && v.status && *reinterpret_cast<volatile int *>(v.status) ==
+                                            int(LCX_ERR_TIMEOUT)) {
+        pre = true;
+        *abort = 1;
+    }
+
+    if (B.u.rows <= 0) {
+        // (a plan that does not fit the tensors: nothing to do)
+        if (threadIdx.x == 0) raise_status(v.status, LCX_ERR_INVALID_ARG);
+    } else if ((warp >> 2) == 3) {
+        setmaxnreg_dec<kRegsIssue>();
+        if (warp == kWarpTma && lane == 0 && B.n > 0 && !p.stall) {
+            // ------------------------------------------------ Q and K producer
+            tma_prefetch_desc(&tmq);
+            tma_prefetch_desc(&tmk);
+            mbar_arrive_expect_tx(&bar.full_q, B.nt * C::kTile);
+            for (int t = 0; t < B.nt; ++t)
+                for (int x = 0; x < D / 64; ++x)
+                    tma_load_4d(smem + t * C::kTile + x * C::kBox, &tmq, &bar.full_q, x * 64,
+                                B.u.q0 + t * B.rstep, B.h0 + t * B.hstep, 0);
+            wait_previous_kernel();                       // the rotated keys
+            uint32_t used = 0;                            // stages with a copy issued
+            bool ok = true;
+            int j = 0;
+            for (; ok && j < B.n; ++j) {
+                const int s = j & mask, r = B.u.k0 + B.tile(j) * kBN;
+                if (j > mask) ok = mbar_wait(&bar.empty_k[s], ((j >> shift) - 1) & 1, abort, tmo);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&bar.full_k[s], (B.precise ? 2 : 1) * C::kTile);
+                for (int x = 0; x < D / 64; ++x) {
+                    tma_load_4d(sK + s * C::kTile + x * C::kBox, &tmk, &bar.full_k[s], x * 64, r,
+                                B.g, 0);
+                    if (B.precise)
+                        tma_load_4d(sK + C::kTile + x * C::kBox, &tml, &bar.full_k[s], x * 64, r,
+                                    B.g, 0);
+                }
+                used |= 1u << s;
+            }
+            // never leave the CTA with copies in flight: the last one of every stage
+            mbar_wait(&bar.full_q, 0, nullptr, tmo);
+            for (int s = 0; s <= mask; ++s)
+                if (used >> s & 1)
+                    mbar_wait(&bar.full_k[s], ((j - 1 - s) >> shift) & 1, nullptr, tmo);
+        } else if (warp == kWarpTmaV && lane == 0 && B.n > 0 && !p.stall) {
+            // ------------------------------------------------ V producer
+            // Border tiles arrive on barriers of their own (full_b), which only the
+            // helpers wait for, one phase after the other: a wait by parity must not
+            // skip phases.  Bit s of a mask: the parity of a stage's next phase.
+            tma_prefetch_desc(&tmv);
+            uint32_t used = 0, used_b = 0, phase = 0, phase_b = 0;
+            bool ok = true;
+            for (int j = 0; ok && j < B.n; ++j) {
+                const int s = j & mask;
+                if (j > mask) ok = mbar_wait(&bar.empty_v[s], ((j >> shift) - 1) & 1, abort, tmo);
+                if (!ok) break;
+                const bool border = is_border(v, B, B.tile(j));
+                uint64_t *full = border ? &bar.full_b[s] : &bar.full_v[s];
+                mbar_arrive_expect_tx(full, C::kTile);
+                for (int x = 0; x < D / 64; ++x)
+                    tma_load_4d(sV + s * C::kTile + x * C::kBox, &tmv, full, x * 64,
+                                B.u.k0 + B.tile(j) * kBN, B.g, 0);
+                (border ? used_b : used) |= 1u << s;
+                (border ? phase_b : phase) ^= 1u << s;
+            }
+            for (int s = 0; s <= mask; ++s) {
+                if (used >> s & 1) mbar_wait(&bar.full_v[s], (phase >> s & 1) ^ 1, nullptr, tmo);
+                if (used_b >> s & 1)
+                    mbar_wait(&bar.full_b[s], (phase_b >> s & 1) ^ 1, nullptr, tmo);
+            }
+        } else if (warp == kWarpMma && lane == 0 && B.n > 0) {
+            // ------------------------------------------------ MMA issuer
+            const uint32_t fmt = p.fp16 ? kFmtF16 : kFmtBF16;
+            const uint32_t id_s = idesc_f32acc(128, kBN, 0, 0, 0, 0) | (fmt << 7) | (fmt << 10);
+            constexpr uint32_t id_pv = idesc_bf16_f32(128, D, 0, 1);   // V as the TMA lands it
+            const uint64_t d0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+            const uint32_t dhi = uint32_t(d0 >> 32), q_lo = uint32_t(d0);
+            const uint32_t k_lo = uint32_t(sdesc_sw128(smem_u32(sK), 16, 1024));
+            const uint32_t ql_lo = uint32_t(sdesc_sw128(smem_u32(smem + C::kOffQLo), 16, 1024));
+            const uint32_t v_lo = uint32_t(sdesc_sw128(smem_u32(sV), C::kBox, 1024));
+            auto product = [&](uint32_t dst, uint32_t qa, uint32_t ka, bool more) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t o = ((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4;
+                    mma_ss_w<0>(dst, qa + o, ka + o, dhi, id_s, more || kk > 0);
+                }
+            };
+            auto issue_s = [&](int t, int s) {
+                const uint32_t dst = tmem + t * kBN, qa = q_lo + ((t * C::kTile) >> 4);
+                const uint32_t ka = k_lo + ((s * C::kTile) >> 4);
+                product(dst, qa, ka, false);
+                if (B.precise) {
+                    product(dst, qa, k_lo + (C::kTile >> 4), true);          // Qh Kl
+                    product(dst, ql_lo + ((t * C::kTile) >> 4), ka, true);   // Ql Kh
+                }
+                mma_commit(&bar.s_ready[t]);
+            };
+            auto issue_pv = [&](int t, int s, bool acc) {
+                const uint32_t va = v_lo + ((s * C::kTile) >> 4);
+                const uint32_t dst = tmem + C::kColO + t * D, pa = tmem + t * kBN;
+#pragma unroll
+                for (int kk = 0; kk < kBN / 16; ++kk)
+                    mma_ts_w<0>(dst, pa + kk * 8, va + ((kk * 16 * 128) >> 4), dhi, id_pv,
+                                acc || kk > 0);
+            };
+            uint32_t cleaned = 0, landed = 0;             // next parity of clean_v, full_v
+            bool ok = mbar_wait(&bar.ready_q, 0, abort, tmo);
+            if (ok) ok = mbar_wait(&bar.full_k[0], 0, abort, tmo);
+            if (ok) {
+                tc_fence_after();
+                for (int t = 0; t < B.nt; ++t) issue_s(t, 0);
+                mma_commit(&bar.empty_k[0]);
+            }
+            for (int j = 0; ok && j < B.n; ++j) {
+                const int s = j & mask, jn = j + 1;
+                if (is_border(v, B, B.tile(j))) {
+                    ok = mbar_wait(&bar.clean_v[s], (cleaned >> s) & 1, abort, tmo);
+                    cleaned ^= 1u << s;
+                } else {
+                    ok = mbar_wait(&bar.full_v[s], (landed >> s) & 1, abort, tmo);
+                    landed ^= 1u << s;
+                }
+                for (int t = 0; ok && t < B.nt; ++t) {
+                    ok = mbar_wait(&bar.p_ready[t], j & 1, abort, tmo);
+                    tc_fence_after();
+                    if (!ok) break;
+                    issue_pv(t, s, j > 0);
+                    if (jn < B.n) {
+                        if (t == 0) {
+                            ok = mbar_wait(&bar.full_k[jn & mask], (jn >> shift) & 1, abort, tmo);
+                            tc_fence_after();
+                            if (!ok) break;
+                        }
+                        issue_s(t, jn & mask);
+                    }
+                }
+                if (ok) {
+                    mma_commit(&bar.empty_v[s]);
+                    if (jn < B.n) mma_commit(&bar.empty_k[jn & mask]);
+                }
+            }
+            if (ok)
+                for (int t = 0; t < B.nt; ++t) mma_commit(&bar.o_ready[t]);
+            // all issued products complete before TMEM is released
+            mma_commit(&bar.drain);
+            mbar_wait(&bar.drain, 0, nullptr, tmo);
+        }
+    } else if ((warp >> 2) == 2) {
+        setmaxnreg_dec<kRegsHelp>();
+        // ------------------------------------------------ helpers
+        const int tw = threadIdx.x - kWarpHelp * 32;
+        bool ok = true;
+        if (B.n > 0) {
+            if (p.fp16) {
+                rotate_queries<D, kHalf>(p, B, tw, smem, bar, abort, tmo, ok);
+                wait_previous_kernel();
+                if (ok && keys_scaled(p, B, tw)) bar.k_scaled = 1;
+            } else {
+                ok = __all_sync(0xffffffffu, mbar_wait(&bar.full_q, 0, abort, tmo));
+            }
+            if (ok) {
+                fence_proxy_async_smem();
+                mbar_arrive(&bar.ready_q);
+            }
+            int nb = 0;
+            uint32_t phase = 0;
+            for (int j = 0; ok && j < B.n; ++j) {
+                const int jt = B.tile(j), s = j & mask;
+                if (!is_border(v, B, jt)) continue;
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait(&bar.full_b[s], (phase >> s) & 1, abort, tmo));
+                phase ^= 1u << s;
+                if (!ok) break;
+                if (nb < kMaxBorder && tw == 0) bar.border_tile[nb] = jt;
+                clean_values<D>(sV + s * C::kTile, tw, jt * kBN + tw >= B.u.nk,
+                                nb < kMaxBorder ? bar.bad[nb] : nullptr, &bar.any_bad);
+                ++nb;
+                fence_proxy_async_smem();
+                mbar_arrive(&bar.clean_v[s]);
+            }
+            if (tw == 0) bar.n_border = nb;
+            mbar_arrive(&bar.helped);
+        }
+    } else {
+        setmaxnreg_inc<kRegsSoftmax>();
+        // ------------------------------------------------ softmax of tile t
+        const int t = warp >> 2, row = (warp & 3) * 32 + lane;
+        if (t < B.nt) {
+            const bool valid = row < B.rows(t);
+            const int pos = B.pos(t) + row, h = B.h0 + t * B.hstep;
+            const long long prow = B.u.q0 + t * B.rstep + row;
+            const uint32_t trow = tmem + (uint32_t((warp & 3) * 32) << 16);
+            const uint32_t s_col = t * kBN, o_col = C::kColO + t * D;
+            float m = -INFINITY, l = 0.f, cl2 = v.c_log2;
+            bool ok = true, scaled = false;
+            if (B.n > 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&bar.ready_q, 0, abort, tmo));
+                if (p.fp16) cl2 *= bar.q_scale[t * kBM + row];
+                scaled = bar.k_scaled != 0;
+            }
+            for (int j = 0; ok && j < B.n; ++j) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&bar.s_ready[t], j & 1, abort, tmo));
+                if (!ok) break;
+                tc_fence_after();
+                const int jt = B.tile(j), k0 = jt * kBN;
+                float x[kBN];
+                tmem_ld128(trow + s_col, x);
+                if (scaled) {
+                    const float *ks = p.k_scale + (long long)(B.u.k0 + k0) * v.Hkv + B.g;
+                    const int last = min(kBN, B.u.nk - k0);
+#pragma unroll
+                    for (int e = 0; e < kBN; ++e)
+                        if (e < last) x[e] *= ks[(long long)e * v.Hkv];
+                }
+                if (!tile_full(v, B, t, jt)) {
+                    // visible: e <= hi and (no window or e >= lo or e < sk)
+                    const int hi = v.causal ? min(pos - k0, B.u.nk - 1 - k0) : B.u.nk - 1 - k0;
+                    const int lo = pos - v.window + 1 - k0, sk = v.sinks - k0;
+                    const bool win = v.window > 0;
+#pragma unroll
+                    for (int e = 0; e < kBN; ++e) {
+                        const bool keep = (e <= hi) & (!win | (e >= lo) | (e < sk));
+                        x[e] = keep ? x[e] : -INFINITY;
+                    }
+                }
+                const float m_new = fmaxf(m, row_max(x) * cl2);
+                const bool need = (m != -INFINITY) && (m_new > m + kLazy);
+                if (__any_sync(0xffffffffu, need)) {
+                    const float alpha = need ? ex2_approx(m - m_new) : 1.f;
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        float o[32];
+                        tmem_ld32(trow + o_col + c * 32, o);
+                        uint32_t u[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * alpha);
+                        tmem_st32_nowait(trow + o_col + c * 32, u);
+                    }
+                    tmem_wait_st();
+                    if (need) {
+                        l *= alpha;
+                        m = m_new;
+                    }
+                }
+                if (m == -INFINITY) m = m_new;
+                const float mref = m == -INFINITY ? 0.f : m;
+                const float2 c2 = make_float2(cl2, cl2), nm2 = make_float2(-mref, -mref);
+                float2 sum = make_float2(0.f, 0.f);
+                uint32_t pk_[kBN / 2];
+#pragma unroll
+                for (int e = 0; e < kBN / 2; ++e) {
+                    const float2 y = fma2(make_float2(x[2 * e], x[2 * e + 1]), c2, nm2);
+                    const float2 w = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                    // P rounded to bf16 for the product; its sum is not
+                    pk_[e] = pack_bf16x2(w.x, w.y);
+                    sum = add2(sum, w);
+                }
+                tmem_st64(trow + s_col, pk_);
+                l += sum.x + sum.y;
+                tc_fence_before();
+                mbar_arrive(&bar.p_ready[t]);
+            }
+            bool bad = false;
+            int nb = 0;
+            if (ok && B.n > 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&bar.o_ready[t], 0, abort, tmo)) &&
+                     __all_sync(0xffffffffu, mbar_wait(&bar.helped, 0, abort, tmo));
+                bad = bar.any_bad != 0;
+                nb = bar.n_border;
+            }
+            if (ok) {
+                tc_fence_after();
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                __nv_bfloat16 *dst =
+                    reinterpret_cast<__nv_bfloat16 *>(v.o) + prow * v.os[0] + h * v.os[1];
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    if (B.n > 0) {
+                        tmem_ld32(trow + o_col + c * 32, o);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] *= inv;
+                    if (bad && valid) {
+                        // non-finite values of border tiles that this row does see
+                        for (int i = 0; i < nb; ++i) {
+                            const bool listed = i < kMaxBorder;
+                            const int jt = listed ? bar.border_tile[i] : -1;
+                            for (int r = 0; listed && r < kBN; ++r) {
+                                if (!(bar.bad[i][r >> 5] >> (r & 31) & 1)) continue;
+                                const int key = jt * kBN + r;
+                                if (key >= B.u.nk || (v.causal && key > pos) ||
+                                    (v.window > 0 && pos - key >= v.window && key >= v.sinks))
+                                    continue;
+                                const __nv_bfloat16 *src =
+                                    reinterpret_cast<const __nv_bfloat16 *>(v.v) +
+                                    (long long)(B.u.k0 + key) * v.vs[0] + B.g * v.vs[1] + c * 32;
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) {
+                                    const float y = static_cast<float>(src[e]);
+                                    if (!(fabsf(y) < INFINITY)) o[e] += y;
+                                }
+                            }
+                        }
+                    }
+                    if (valid) {
+                        uint4 *out = reinterpret_cast<uint4 *>(dst + c * 32);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            out[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]),
+                                                pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                                                pack_bf16x2(o[8 * e + 4], o[8 * e + 5]),
+                                                pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+                    }
+                }
+                if (valid && v.lse)
+                    v.lse[(long long)h * v.Tq + prow] =
+                        l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+            }
+        }
+    }
+
+    __syncthreads();
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (threadIdx.x == 0) {
+        // (a CTA without key tiles, too, ends after the key rotation: what follows in
+        // the stream may write its inputs)
+        wait_previous_kernel();
+        if (!pre && bar.abort) raise_status(v.status, LCX_ERR_TIMEOUT);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = []() -> EncodeTiledFn {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        return reinterpret_cast<EncodeTiledFn>(ptr);
+    }();
+    return fn;
+}
+
+// [T, H, D] tensor of 16-bit elements -> boxes of 64 columns x 128 rows, 128-byte
+// swizzle; rows past T read as zero.
+lcx_status token_map(CUtensorMap *map, const void *ptr, int64_t T, int64_t H, int64_t D,
+                     const long long *st, const char *name) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return fail(LCX_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+    const cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(T), cuuint64_t(H), 1};
+    const cuuint64_t strides[3] = {cuuint64_t(st[0] * 2), cuuint64_t(st[1] * 2), 16};
+    const cuuint32_t box[4] = {64, 128, 1, 1}, ones[4] = {1, 1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims,
+                          strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(LCX_ERR_UNSUPPORTED, "tensor map for %s rejected (CUresult %d)", name, int(r));
+    return LCX_OK;
+}
+
+// Workspace of rotated keys: fp32, or the parts the tcgen05 kernel reads.
+struct KeySpace {
+    int64_t lo, scale, flags, bytes;      // offsets (hi, or the fp32 keys, at 0)
+};
+KeySpace key_space(int64_t total_k, int64_t H, int64_t D, int dtype) {
+    auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+    KeySpace k = {};
+    if (dtype == LCX_F32) {
+        k.bytes = up(total_k * H * D * 4);
+        return k;
+    }
+    k.lo = up(total_k * H * D * 2);
+    k.scale = k.lo + up(total_k * H * D * 2);
+    k.flags = k.scale + up(total_k * H * 4);
+    k.bytes = k.flags + up((total_k / 16 + 1) * 4);
+    return k;
+}
+
+template <int D, bool kHalf>
+lcx_status launch_keys(KeyParams &k, cudaStream_t s) {
+    constexpr int rpc = kKeyThreads / Job<D, kHalf>::CPR;
+    varlen_keys_kernel<D, kHalf><<<unsigned((k.T + rpc - 1) / rpc), kKeyThreads, 0, s>>>(k);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return fail(LCX_ERR_CUDA, "attn_varlen key launch failed: %s", cudaGetErrorString(e));
+    return LCX_OK;
+}
+
+template <int D, bool kHalf>
+lcx_status launch_tc(const CUtensorMap (&m)[4], TcParams &p, bool after_keys, cudaStream_t s) {
+    auto kern = varlen_kernel<D, kHalf>;
+    p.flag_rows = kKeyThreads / Job<D, kHalf>::CPR;
+    // the warpgroups' register shares must add up to what the launch holds
+    static const int regs = []() {
+        cudaFuncAttributes fa;
+        return cudaFuncGetAttributes(&fa, varlen_kernel<D, kHalf>) == cudaSuccess ? fa.numRegs : -1;
+    }();
+    if (regs * kThreads < (2 * kRegsSoftmax + kRegsHelp + kRegsIssue) * 128)
+        return fail(LCX_ERR_CUDA, "attn_varlen kernel built with %d registers per thread; the "
+                    "warpgroup register split needs 128", regs);
+    cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<D>::kSmem);
+    if (e != cudaSuccess)
+        return fail(LCX_ERR_CUDA, "cudaFuncSetAttribute failed: %s", cudaGetErrorString(e));
+    const long long grid = (long long)p.v.n_units * p.head_units;
+    if (grid > 0x7fffffffLL) return fail(LCX_ERR_UNSUPPORTED, "too many work units");
+    if (after_keys)
+        e = launch_dependent(kern, dim3(unsigned(grid)), dim3(kThreads), Tc<D>::kSmem, s, m[0],
+                             m[1], m[2], m[3], p);
+    else
+        kern<<<unsigned(grid), kThreads, Tc<D>::kSmem, s>>>(m[0], m[1], m[2], m[3], p);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return fail(LCX_ERR_CUDA, "attn_varlen launch failed: %s", cudaGetErrorString(e));
+    return LCX_OK;
+}
+
+// The bf16 path: rotated keys (unless given), then the tcgen05 kernel.
+lcx_status run_tc(const lcx_varlen_args *a, const VarlenParams &v, cudaStream_t s) {
+    const lcx_varlen_info &I = a->info;
+    const bool half = v.half != 0, rotate = v.rotate_q != 0;
+    TcParams p;
+    memset(&p, 0, sizeof(p));
+    p.v = v;
+    p.fp16 = rotate ? 1 : 0;
+    p.stall = (a->flags & LCX_VARLEN_TEST_STALL) ? 1 : 0;
+    // Two query tiles per CTA when those CTAs still cover the SMs; a problem of few
+    // row blocks runs faster over twice the CTAs, one tile each.
+    const int64_t pairs = v.G % 2 == 0 ? I.n_units[0] * (v.Hq / 2) : I.n_units[1] * v.Hq;
+    p.mode = pairs < device_sms() ? kOneTile : v.G % 2 == 0 ? kTwoHeads : kTwoBlocks;
+    p.head_units = p.mode == kTwoHeads ? v.Hq / 2 : v.Hq;
+    const int which = p.mode == kTwoBlocks;
+    p.v.units =
+        reinterpret_cast<const VarlenUnit *>(a->plan + plan_units(I.n_seqs, which, I.n_units[0]));
+    p.v.n_units = int(I.n_units[which]);
+    const void *kp = a->k, *lo = a->k;
+    long long ks[2] = {v.ks[0], v.ks[1]};
+    if (rotate && I.total_k > 0) {
+        const KeySpace ws = key_space(I.total_k, v.Hkv, a->D, LCX_BF16);
+        char *base = static_cast<char *>(a->workspace);
+        KeyParams k = {};
+        k.k = static_cast<const __nv_bfloat16 *>(a->k);
+        k.st = a->k_strides[0];
+        k.sh = a->k_strides[1];
+        k.hi = reinterpret_cast<__half *>(base);
+        k.lo = reinterpret_cast<__half *>(base + ws.lo);
+        k.scale = reinterpret_cast<float *>(base + ws.scale);
+        k.flags = reinterpret_cast<int *>(base + ws.flags);
+        k.cu = a->plan + plan_cu_k(I.n_seqs);
+        k.n = int(I.n_seqs);
+        k.T = int(I.total_k);
+        k.H = v.Hkv;
+        k.all_lo = v.window > 0 && v.window < 128;
+        rope_freqs_unchecked(&a->rope, effective_seq_len(&a->rope, std::max<int64_t>(I.max_k, 1)),
+                             k.theta, &k.ms);
+        lcx_status st = a->D == 128 ? (half ? launch_keys<128, true>(k, s) : launch_keys<128, false>(k, s))
+                                    : (half ? launch_keys<64, true>(k, s) : launch_keys<64, false>(k, s));
+        if (st != LCX_OK) return st;
+        kp = k.hi;
+        lo = k.lo;
+        p.k_scale = k.scale;
+        p.k_flags = k.flags;
+    }
+    CUtensorMap m[4];
+    lcx_status st;
+    if ((st = token_map(&m[0], a->q, a->Tq, v.Hq, a->D, v.qs, "q")) != LCX_OK) return st;
+    if (I.total_k > 0) {
+        if ((st = token_map(&m[1], kp, v.Tk, v.Hkv, a->D, ks, "k")) != LCX_OK) return st;
+        if ((st = token_map(&m[2], lo, v.Tk, v.Hkv, a->D, ks, "k")) != LCX_OK) return st;
+        if ((st = token_map(&m[3], a->v, a->Tk, v.Hkv, a->D, v.vs, "v")) != LCX_OK) return st;
+    } else {
+        m[1] = m[2] = m[3] = m[0];      // no block has a key tile
+    }
+    const bool dep = p.k_scale != nullptr;
+    if (a->D == 128)
+        return half ? launch_tc<128, true>(m, p, dep, s) : launch_tc<128, false>(m, p, dep, s);
+    return half ? launch_tc<64, true>(m, p, dep, s) : launch_tc<64, false>(m, p, dep, s);
+}
+
 // Sums over the sequences; false for lengths outside the limits.
 bool plan_sums(const int32_t *lq, const int32_t *lk, int64_t n, lcx_varlen_info *x) {
     memset(x, 0, sizeof(*x));
@@ -249,8 +1228,10 @@ lcx_status varlen_prepare(const lcx_varlen_args *a, VarlenParams &p, bool *noop)
         return fail(LCX_ERR_INVALID_ARG, "window and sinks must be >= 0");
     if (!a->causal && (a->window != 0 || a->sinks != 0))
         return fail(LCX_ERR_UNSUPPORTED, "window / sinks need causal attention");
-    if (a->flags & ~uint32_t(LCX_VARLEN_PREROTATED))
+    if (a->flags & ~uint32_t(LCX_VARLEN_PREROTATED | LCX_VARLEN_TEST_STALL))
         return fail(LCX_ERR_INVALID_ARG, "unknown flags");
+    if ((a->flags & LCX_VARLEN_TEST_STALL) && a->dtype != LCX_BF16)
+        return fail(LCX_ERR_UNSUPPORTED, "the stall test hook needs bf16 operands");
     if (a->reserved0 != 0) return fail(LCX_ERR_INVALID_ARG, "reserved0 must be 0");
     if (a->watchdog_ms < 0 || a->watchdog_ms > 60000)
         return fail(LCX_ERR_INVALID_ARG, "watchdog_ms must be in [0, 60000]");
@@ -279,16 +1260,17 @@ lcx_status varlen_prepare(const lcx_varlen_args *a, VarlenParams &p, bool *noop)
     }
     const bool rotate = !(a->flags & LCX_VARLEN_PREROTATED) && a->rope.mode != LCX_ROPE_NONE;
     if (rotate && I.total_k > 0) {
-        if (!a->k_rot || !aligned16(a->k_rot))
-            return fail(LCX_ERR_INVALID_ARG, "k_rot must be a 16-byte aligned device pointer");
-        const int64_t need = I.total_k * a->Hkv * a->D * es;
-        if (a->k_rot_bytes < need)
-            return fail(LCX_ERR_INVALID_ARG, "k_rot holds %lld bytes; %lld needed",
-                        (long long)a->k_rot_bytes, (long long)need);
+        if (!a->workspace || (reinterpret_cast<uintptr_t>(a->workspace) & 255u))
+            return fail(LCX_ERR_INVALID_ARG,
+                        "workspace must be a 256-byte aligned device pointer");
+        const int64_t need = key_space(I.total_k, a->Hkv, a->D, a->dtype).bytes;
+        if (a->workspace_bytes < need)
+            return fail(LCX_ERR_INVALID_ARG, "workspace holds %lld bytes; %lld needed",
+                        (long long)a->workspace_bytes, (long long)need);
     }
     memset(&p, 0, sizeof(p));
     p.q = static_cast<const char *>(a->q);
-    p.k = static_cast<const char *>(rotate ? a->k_rot : a->k);
+    p.k = static_cast<const char *>(rotate ? a->workspace : a->k);
     p.v = static_cast<const char *>(a->v);
     p.o = static_cast<char *>(a->o);
     p.lse = a->lse;
@@ -394,17 +1376,23 @@ extern "C" lcx_status lcx_attn_varlen(const lcx_varlen_args *a, void *stream) {
     lcx_status st = varlen_prepare(a, p, &noop);
     if (st != LCX_OK || noop) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (a->dtype == LCX_BF16) return run_tc(a, p, s);
     if (p.rotate_q) {
         st = rotate_packed(&a->rope, std::max<int64_t>(a->info.max_k, 1), a->k, a->k_strides,
-                           a->k_rot, a->dtype, a->plan + plan_cu_k(a->info.n_seqs),
+                           a->workspace, a->dtype, a->plan + plan_cu_k(a->info.n_seqs),
                            int(a->info.n_seqs), a->info.total_k, a->Hkv, a->D, s);
         if (st != LCX_OK) return st;
     }
     p.units = reinterpret_cast<const VarlenUnit *>(
         a->plan + plan_units(a->info.n_seqs, 0, a->info.n_units[0]));
     p.n_units = int(a->info.n_units[0]);
-    if (a->dtype == LCX_BF16)
-        return a->D == 128 ? launch_simt<__nv_bfloat16, 128>(p, s)
-                           : launch_simt<__nv_bfloat16, 64>(p, s);
     return a->D == 128 ? launch_simt<float, 128>(p, s) : launch_simt<float, 64>(p, s);
+}
+
+extern "C" int64_t lcx_varlen_workspace_bytes(const lcx_varlen_info *info, int64_t Hkv, int64_t D,
+                                              int32_t dtype) {
+    if (!info || info->total_k < 0 || info->total_k > (1 << 30) || Hkv <= 0 || Hkv > 65536 ||
+        (D != 64 && D != 128) || (dtype != LCX_BF16 && dtype != LCX_F32))
+        return -1;
+    return key_space(info->total_k, Hkv, D, dtype).bytes;
 }

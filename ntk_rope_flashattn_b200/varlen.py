@@ -12,6 +12,7 @@ from . import RopeParams, _check, _dtype_code, _RopeParams, _same_device, load
 from .paged import _rope_c, _strides3
 
 LCX_VARLEN_PREROTATED = 1
+LCX_VARLEN_TEST_STALL = 0x80000000
 
 _P, _I64, _I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
 
@@ -23,7 +24,7 @@ class _Info(ctypes.Structure):
 
 class _VarlenArgs(ctypes.Structure):
     _fields_ = [("q", _P), ("k", _P), ("v", _P), ("o", _P), ("lse", _P), ("plan", _P),
-                ("k_rot", _P), ("k_rot_bytes", _I64), ("dev_status", _P), ("info", _Info),
+                ("workspace", _P), ("workspace_bytes", _I64), ("dev_status", _P), ("info", _Info),
                 ("dtype", _I32), ("causal", _I32), ("Tq", _I64), ("Tk", _I64), ("Hq", _I64),
                 ("Hkv", _I64), ("D", _I64), ("q_strides", _I64 * 3), ("k_strides", _I64 * 3),
                 ("v_strides", _I64 * 3), ("o_strides", _I64 * 3), ("rope", _RopeParams),
@@ -36,6 +37,8 @@ def _declare(lib):
     lib.lcx_varlen_plan_ints.restype = _I64
     lib.lcx_varlen_plan.argtypes = [_P, _P, _I64, _P, _I64, ctypes.POINTER(_Info)]
     lib.lcx_varlen_plan.restype = ctypes.c_int
+    lib.lcx_varlen_workspace_bytes.argtypes = [ctypes.POINTER(_Info), _I64, _I64, _I32]
+    lib.lcx_varlen_workspace_bytes.restype = _I64
     lib.lcx_attn_varlen.argtypes = [ctypes.POINTER(_VarlenArgs), _P]
     lib.lcx_attn_varlen.restype = ctypes.c_int
 
@@ -91,10 +94,22 @@ class VarlenPlan:
         return self.plan[9 + n:9 + n + n + 1]
 
 
+def varlen_workspace_bytes(plan: VarlenPlan, kv_heads: int, head_dim: int, dtype) -> int:
+    """Workspace bytes of ``attn_varlen`` (lcx_varlen_workspace_bytes)."""
+    import torch
+    code = {torch.bfloat16: 0, torch.float32: 1}.get(dtype, -1)
+    need = int(load().lcx_varlen_workspace_bytes(ctypes.byref(plan.info), int(kv_heads),
+                                                 int(head_dim), code))
+    if need < 0:
+        raise ValueError("attn_varlen: %s kv heads, head_dim %s, %s are not supported" %
+                         (kv_heads, head_dim, dtype))
+    return need
+
+
 def attn_varlen(q, k, v, plan: VarlenPlan, rope: RopeParams, causal: bool = True, window: int = 0,
                 sinks: int = 0, softmax_scale: float = 0.0, return_lse: bool = False,
-                prerotated: bool = False, out=None, lse=None, k_rot=None, status=None,
-                watchdog_ms: int = 0):
+                prerotated: bool = False, out=None, lse=None, workspace=None, status=None,
+                watchdog_ms: int = 0, _test_stall: bool = False):
     """Fused RoPE + causal attention over the plan's packed sequences.
 
     q [Tq, Hq, D], k/v [Tk, Hkv, D] CUDA tensors (bf16 or fp32, last dim
@@ -104,7 +119,9 @@ def attn_varlen(q, k, v, plan: VarlenPlan, rope: RopeParams, causal: bool = True
     were (zero when the call allocates o and lse itself).  ``prerotated``: q and k
     are already rotated
     (``paged_append``'s q_out and k_out); otherwise the keys are rotated once into
-    ``k_rot`` (allocated when not given).  A query without a visible key gets
+    ``workspace`` (uint8, 256-byte aligned, ``varlen_workspace_bytes``; allocated when
+    not given; calls in flight at the same time, replayed graphs among them, must not
+    share one).  A query without a visible key gets
     o = 0 and lse = -inf.  ``status`` and ``watchdog_ms`` as for ``attn_fwd``."""
     import torch
     for t in (q, k, v):
@@ -116,7 +133,7 @@ def attn_varlen(q, k, v, plan: VarlenPlan, rope: RopeParams, causal: bool = True
         raise ValueError("shape mismatch: q %s k %s v %s" % (q.shape, k.shape, v.shape))
     if not (q.dtype == k.dtype == v.dtype):
         raise ValueError("q, k, v must share a dtype")
-    _same_device(q, k=k, v=v, out=out, lse=lse, k_rot=k_rot, status=status, plan=plan.plan)
+    _same_device(q, k=k, v=v, out=out, lse=lse, workspace=workspace, status=status, plan=plan.plan)
     whole = plan.total_q == Tq
     alloc = torch.empty if whole else torch.zeros
     o = out if out is not None else alloc((Tq, Hq, D), dtype=q.dtype, device=q.device)
@@ -134,12 +151,11 @@ def attn_varlen(q, k, v, plan: VarlenPlan, rope: RopeParams, causal: bool = True
     a.lse = None if lse is None else lse.data_ptr()
     a.plan, a.info = plan.plan.data_ptr(), plan.info
     a.dev_status = None if status is None else status.data_ptr()
-    if not prerotated and rope.mode != "none" and k_rot is None:
-        k_rot = torch.empty((max(plan.total_k, 1), Hkv, D), dtype=k.dtype, device=k.device)
-    if k_rot is not None:
-        if not k_rot.is_contiguous():
-            raise ValueError("k_rot must be contiguous")
-        a.k_rot, a.k_rot_bytes = k_rot.data_ptr(), k_rot.numel() * k_rot.element_size()
+    if not prerotated and rope.mode != "none" and workspace is None:
+        workspace = torch.empty(max(varlen_workspace_bytes(plan, Hkv, D, k.dtype), 1),
+                                dtype=torch.uint8, device=k.device)
+    if workspace is not None:
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.nbytes
     a.dtype, a.causal = _dtype_code(q), 1 if causal else 0
     a.Tq, a.Tk, a.Hq, a.Hkv, a.D = Tq, Tk, Hq, Hkv, D
     a.q_strides, a.k_strides = _strides3(q), _strides3(k)
@@ -147,7 +163,8 @@ def attn_varlen(q, k, v, plan: VarlenPlan, rope: RopeParams, causal: bool = True
     rope_c = _rope_c(rope)
     a.rope = rope_c
     a.window, a.sinks, a.softmax_scale = int(window), int(sinks), float(softmax_scale)
-    a.flags = LCX_VARLEN_PREROTATED if prerotated else 0
+    a.flags = ((LCX_VARLEN_PREROTATED if prerotated else 0) |
+               (LCX_VARLEN_TEST_STALL if _test_stall else 0))
     a.watchdog_ms = int(watchdog_ms)
     with torch.cuda.device(q.device):
         _check(load().lcx_attn_varlen(ctypes.byref(a), torch.cuda.current_stream().cuda_stream))

@@ -30,11 +30,12 @@ def plain(q, k, v, lq, lk, rope, causal=True, window=0, sinks=0, scale=None, pre
 
 
 def arithmetic(dtype, n):
-    """(u_s, u_p): bf16 rounds q', k' and the weights (the sums run over the unrounded
-    weights); fp32 rounds nothing but its sums (and q', k' to fp32)."""
-    acc = 128 * 2.0 ** -24 + 2.0 ** -21
+    """(u_s, u_p): bf16 inputs: q' and k' rounded to fp16 (2^-11 each), their products'
+    sums cut by the tensor core, the weights rounded to bf16 (their sum is not); fp32
+    rounds nothing but its sums (and q', k' to fp32)."""
+    acc = 128 * 2.0 ** -23 + 2.0 ** -18
     if dtype == torch.bfloat16:
-        return 2.0 ** -7 + 2.0 ** -16 + acc, 2.0 ** -8 + n * 2.0 ** -24 + 2.0 ** -20
+        return 2.0 ** -10 + 2.0 ** -20 + acc, 2.0 ** -8 + n * 2.0 ** -23 + 2.0 ** -20
     return 2.0 ** -22 + acc, n * 2.0 ** -24 + 2.0 ** -20
 
 
@@ -187,16 +188,18 @@ def test_replays_from_a_graph_and_other_streams():
     rope = lcx.RopeParams("plain", 64)
     plan = lcx.VarlenPlan([77, 200])
     q, k, v = (randn(i, 277, h, 64) for i, h in ((1, 4), (2, 2), (3, 2)))
-    k_rot, out = torch.empty_like(k), torch.empty_like(q)
+    out = torch.empty_like(q)
+    ws = torch.empty(lcx.varlen_workspace_bytes(plan, 2, 64, k.dtype), dtype=torch.uint8,
+                     device="cuda")
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
-        lcx.attn_varlen(q, k, v, plan, rope, k_rot=k_rot, out=out)
+        lcx.attn_varlen(q, k, v, plan, rope, workspace=ws, out=out)
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(out, lcx.attn_varlen(q, k, v, plan, rope))
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
-        lcx.attn_varlen(q, k, v, plan, rope, k_rot=k_rot, out=out)
+        lcx.attn_varlen(q, k, v, plan, rope, workspace=ws, out=out)
     for i in range(3):
         for t in (q, k, v):
             t.copy_(randn(10 * i + t.shape[1], *t.shape))
@@ -211,3 +214,60 @@ def test_a_plan_that_is_not_the_tensors_is_refused():
         lcx.attn_varlen(q, k, k, lcx.VarlenPlan([11]), rope)
     with pytest.raises(ValueError):
         lcx.attn_varlen(q, k, k, lcx.VarlenPlan([10], device="cpu"), rope)
+
+
+def test_expired_waits_report_timeout_and_context_survives():
+    """With no copies issued every wait runs out: the kernel ends on its own, reports
+    LCX_ERR_TIMEOUT and leaves the context usable."""
+    rope = lcx.RopeParams("plain", 128)
+    plan = lcx.VarlenPlan([300, 40])
+    q, k, v = (randn(i, 340, h, 128) for i, h in ((1, 4), (2, 2), (3, 2)))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lcx.attn_varlen(q, k, v, plan, rope, status=status, watchdog_ms=50, _test_stall=True)
+    torch.cuda.synchronize()
+    assert int(status) == lcx.LCX_ERR_TIMEOUT
+    status.zero_()
+    o, lse = lcx.attn_varlen(q, k, v, plan, rope, status=status, return_lse=True)
+    assert int(status) == 0
+    compare(o, lse, plain(q, k, v, [300, 40], [300, 40], rope), torch.bfloat16, 300)
+
+
+@pytest.mark.parametrize("Hq,H", [(2, 1), (3, 1)])
+def test_values_far_outside_fp16(Hq, H):
+    """Rows of q and k of any bf16 magnitude: rows beyond fp16's range are scaled, the
+    others keep their bits of precision."""
+    rope = lcx.RopeParams("plain", 64)
+    lens = [150, 400]
+    plan = lcx.VarlenPlan(lens)
+    q, k, v = (randn(i, 550, h, 64) for i, h in ((1, Hq), (2, H), (3, H)))
+    # queries down as far as their keys are up, so the logits stay of ordinary size
+    qs, ks = q.clone(), k.clone()
+    ks[:150] = (k[:150].float() * 2.0 ** 30).bfloat16()
+    qs[:150] = (q[:150].float() * 2.0 ** -30).bfloat16()
+    ks[150:] = (k[150:].float() * 2.0 ** -25).bfloat16()
+    qs[150:] = (q[150:].float() * 2.0 ** 25).bfloat16()
+    o, lse = lcx.attn_varlen(qs, ks, v, plan, rope, return_lse=True)
+    compare(o, lse, plain(qs, ks, v, lens, lens, rope), torch.bfloat16, 400)
+    # one key row in a hundred far up, met by queries far down
+    ks, qs = k.clone(), (q.float() * 2.0 ** -20).bfloat16()
+    ks[::100] = (k[::100].float() * 2.0 ** 20).bfloat16()
+    o, lse = lcx.attn_varlen(qs, ks, v, plan, rope, return_lse=True)
+    compare(o, lse, plain(qs, ks, v, lens, lens, rope), torch.bfloat16, 400)
+
+
+def test_lse_of_short_rows_is_precise():
+    """fp16 operands, in two parts where a row sees few keys: lse stays within 3e-5
+    of exact for rows of 1 to 127 keys (u_s = 2^-21 for two parts of both factors;
+    E < 20 for N(0, 1) inputs at D = 128) and windows below 128 keys."""
+    rope = lcx.RopeParams("plain", 128)
+    lens = [1, 2, 60, 127, 300]
+    n = sum(lens)
+    plan = lcx.VarlenPlan(lens)
+    q, k, v = (randn(i, n, h, 128) for i, h in ((1, 4), (2, 2), (3, 2)))
+    o, lse = lcx.attn_varlen(q, k, v, plan, rope, return_lse=True)
+    w = plain(q, k, v, lens, lens, rope)
+    short = torch.cat([torch.arange(x) < 127 for x in lens])
+    assert ((lse.double().cpu() - w[1]).abs()[:, short]).max() <= 3e-5
+    o, lse = lcx.attn_varlen(q, k, v, plan, rope, window=9, sinks=1, return_lse=True)
+    w = plain(q, k, v, lens, lens, rope, True, 9, 1)
+    assert (lse.double().cpu() - w[1]).abs().max() <= 3e-5

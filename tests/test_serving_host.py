@@ -235,8 +235,8 @@ def test_decode_workspace(lib):
 
 def varlen_args(**kw):
     a = varlen._VarlenArgs()
-    a.q = a.k = a.v = a.o = a.plan = a.k_rot = F
-    a.k_rot_bytes = 1 << 30
+    a.q = a.k = a.v = a.o = a.plan = a.workspace = F
+    a.workspace_bytes = 1 << 30
     a.info = lcx.VarlenPlan([100, 28], device="cpu").info
     a.causal, a.Tq, a.Tk, a.Hq, a.Hkv, a.D = 1, 128, 128, 8, 4, 128
     a.q_strides = a.o_strides = (ctypes.c_int64 * 3)(8 * 128, 128, 1)
@@ -256,7 +256,7 @@ def varlen_args(**kw):
     (dict(causal=0, window=5), UNS), (dict(flags=2), BAD), (dict(reserved0=1), BAD),
     (dict(watchdog_ms=60001), BAD), (dict(softmax_scale=float("inf")), BAD), (dict(plan=0), BAD),
     (dict(plan=F + 4), BAD), (dict(q=F + 2), UNS), (dict(v=0), BAD), (dict(o=0), BAD),
-    (dict(k_rot=0), BAD), (dict(k_rot_bytes=1000), BAD), (dict(rope=rope(64)), UNS),
+    (dict(workspace=0), BAD), (dict(workspace_bytes=1000), BAD), (dict(workspace=F + 16), BAD), (dict(rope=rope(64)), UNS),
     (dict(q_strides=[1024, 128, 2]), UNS), (dict(k_strides=[512, 100, 1]), UNS),
 ])
 def test_varlen_refusals(lib, kw, expect):
