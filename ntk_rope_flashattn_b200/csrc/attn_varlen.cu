@@ -270,20 +270,23 @@ __device__ __forceinline__ float range_scale(float amax, float *undo) {
     return __uint_as_float(uint32_t(127 - e) << 23);
 }
 
-// 8 values as fp16 parts and (when wanted) remainders.
-__device__ __forceinline__ uint4 half_parts(const float (&y)[8], bool want_lo, uint4 *lo) {
-    uint32_t h[4], l[4];
+// 8 values as fp16 parts, and the remainders of such parts.
+__device__ __forceinline__ uint4 half_parts(const float (&y)[8]) {
+    return make_uint4(pack_f16x2(y[0], y[1]), pack_f16x2(y[2], y[3]), pack_f16x2(y[4], y[5]),
+                      pack_f16x2(y[6], y[7]));
+}
+__device__ __forceinline__ uint4 half_rest(const float (&y)[8], const uint4 &hi) {
+    const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w};
+    uint32_t l[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        h[e] = pack_f16x2(y[2 * e], y[2 * e + 1]);
         const float2 f = f16x2_to_f32x2(h[e]);
         float a = y[2 * e] - f.x, b = y[2 * e + 1] - f.y;
         a = a == a ? a : 0.f;                 // an infinite value has no remainder
         b = b == b ? b : 0.f;
-        l[e] = want_lo ? pack_f16x2(a, b) : 0u;
+        l[e] = pack_f16x2(a, b);
     }
-    *lo = make_uint4(l[0], l[1], l[2], l[3]);
-    return make_uint4(h[0], h[1], h[2], h[3]);
+    return make_uint4(l[0], l[1], l[2], l[3]);
 }
 
 __device__ __forceinline__ float abs_max8(const float (&x)[8]) {
@@ -394,12 +397,13 @@ __global__ void __launch_bounds__(kKeyThreads)
             }
             if (!in || b + u >= p.H) continue;
             const long long at = ((long long)t * p.H + b + u) * D;
-            uint4 lo;
-            *reinterpret_cast<uint4 *>(p.hi + at + e1) = half_parts(x1, want_lo, &lo);
-            if (want_lo) *reinterpret_cast<uint4 *>(p.lo + at + e1) = lo;
+            const uint4 h1 = half_parts(x1);
+            *reinterpret_cast<uint4 *>(p.hi + at + e1) = h1;
+            if (want_lo) *reinterpret_cast<uint4 *>(p.lo + at + e1) = half_rest(x1, h1);
             if (kHalf) {
-                *reinterpret_cast<uint4 *>(p.hi + at + e2) = half_parts(x2, want_lo, &lo);
-                if (want_lo) *reinterpret_cast<uint4 *>(p.lo + at + e2) = lo;
+                const uint4 h2 = half_parts(x2);
+                *reinterpret_cast<uint4 *>(p.hi + at + e2) = h2;
+                if (want_lo) *reinterpret_cast<uint4 *>(p.lo + at + e2) = half_rest(x2, h2);
             }
             if (q == 0) p.scale[(long long)t * p.H + b + u] = undo;
         }
@@ -428,6 +432,7 @@ struct TcParams {
     int mode, fp16;                 // fp16: rotated operands; 0: bf16 inputs as they are
     int head_units;                 // CTAs per row block
     int stall;                      // the producers issue nothing (watchdog test hook)
+    float2 step[64];                // cos, sin of the angle between a thread's rows
 };
 
 template <int D>
@@ -536,68 +541,69 @@ __device__ __forceinline__ float row_max(const float (&v)[128]) {
     return fmaxf(max3(m0, m1, m2), m3);
 }
 
-// The query tiles rotated in shared memory: bf16 -> fp16 parts (and, precise,
-// remainders), one scale per row.  The helper thread handles pairs of one job and
-// rows r0 + RP k, and steps its angles by RP positions (at most 16 steps: 2^-19).
+// The query tiles rotated in shared memory by the 256 softmax threads: bf16 -> fp16
+// parts (and, precise, remainders), one scale per row.  A thread handles the pairs
+// of one job in every RP-th row; two tiles of the same rows share the angles, which
+// step by RP positions (at most 15 steps of 2^-23 each).
 template <int D, bool kHalf>
-__device__ __forceinline__ void rotate_queries(const TcParams &p, const Block &b, int tw,
+__device__ __forceinline__ void rotate_queries(const TcParams &p, const Block &b, int tid,
                                                uint8_t *smem, Bars<Tc<D>::NS> &bar,
                                                volatile int *abort, uint64_t tmo, bool &ok) {
     using J = Job<D, kHalf>;
-    constexpr int RP = 128 / J::CPR;
-    const int q = tw % J::CPR, r0 = tw / J::CPR;
+    constexpr int RP = 256 / J::CPR;
+    const int q = tid % J::CPR, r0 = tid / J::CPR;
+    const bool two_blocks = b.rstep != 0 && b.nt == 2;
+    const int rows = two_blocks ? 2 * kBM : kBM, both = two_blocks ? 1 : b.nt;
     float c[J::PPJ], s[J::PPJ], sc[J::PPJ], ss[J::PPJ];
-    for (int t = 0; t < b.nt; ++t) {
-        // two heads: the same rows, so the same angles; turn both tiles together
-        if (t == 1 && b.rstep == 0) break;
-        const int both = b.rstep == 0 ? b.nt : 1;
+#pragma unroll
+    for (int e = 0; e < J::PPJ; ++e) {
+        __sincosf(rope_reduced_angle((long long)b.u.pos0 + r0, p.v.theta[q * J::PPJ + e]), &s[e],
+                  &c[e]);
+        sc[e] = p.step[q * J::PPJ + e].x;
+        ss[e] = p.step[q * J::PPJ + e].y;
+    }
+    ok = __all_sync(0xffffffffu, mbar_wait(&bar.full_q, 0, abort, tmo));
+    if (!ok) return;
+#pragma unroll 1
+    for (int R = r0; R < rows; R += RP) {
+        const int r = R & (kBM - 1), t0 = R >> 7;
+#pragma unroll 1
+        for (int x = 0; x < both; ++x) {
+            uint8_t *tile = smem + (t0 + x) * Tc<D>::kTile;
+            const uint32_t oa = chunk_off(r, q), ob = chunk_off(r, q + D / 16);
+            float x1[8], x2[8];
+            unpack(*reinterpret_cast<const uint4 *>(tile + oa), x1);
+            if constexpr (kHalf) unpack(*reinterpret_cast<const uint4 *>(tile + ob), x2);
+            turn<kHalf>(x1, x2, c, s);
+            float mx = kHalf ? fmaxf(abs_max8(x1), abs_max8(x2)) : abs_max8(x1);
+#pragma unroll
+            for (int o = 1; o < J::CPR; o <<= 1)
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            float undo;
+            const float f = range_scale(mx, &undo);
+            if (undo != 1.f) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x1[e] *= f;
+                    if constexpr (kHalf) x2[e] *= f;
+                }
+            }
+            if (q == 0) bar.q_scale[(t0 + x) * kBM + r] = undo;
+            uint8_t *low = smem + Tc<D>::kOffQLo + (t0 + x) * Tc<D>::kTile;
+            const uint4 h1 = half_parts(x1);
+            *reinterpret_cast<uint4 *>(tile + oa) = h1;
+            if (b.precise) *reinterpret_cast<uint4 *>(low + oa) = half_rest(x1, h1);
+            if constexpr (kHalf) {
+                const uint4 h2 = half_parts(x2);
+                *reinterpret_cast<uint4 *>(tile + ob) = h2;
+                if (b.precise) *reinterpret_cast<uint4 *>(low + ob) = half_rest(x2, h2);
+            }
+        }
 #pragma unroll
         for (int e = 0; e < J::PPJ; ++e) {
-            const double th = p.v.theta[q * J::PPJ + e];
-            __sincosf(rope_reduced_angle((long long)b.pos(t) + r0, th), &s[e], &c[e]);
-            __sincosf(rope_reduced_angle((long long)RP, th), &ss[e], &sc[e]);
-        }
-        if (t == 0) ok = __all_sync(0xffffffffu, mbar_wait(&bar.full_q, 0, abort, tmo));
-        if (!ok) return;
-#pragma unroll 1
-        for (int k = 0; k < 128 / RP; ++k) {
-            const int r = r0 + k * RP;
-            for (int x = 0; x < both; ++x) {
-                uint8_t *tile = smem + (t + x) * Tc<D>::kTile;
-                const uint32_t oa = chunk_off(r, q), ob = chunk_off(r, q + D / 16);
-                float x1[8], x2[8];
-                unpack(*reinterpret_cast<const uint4 *>(tile + oa), x1);
-                if constexpr (kHalf) unpack(*reinterpret_cast<const uint4 *>(tile + ob), x2);
-                turn<kHalf>(x1, x2, c, s);
-                float mx = kHalf ? fmaxf(abs_max8(x1), abs_max8(x2)) : abs_max8(x1);
-#pragma unroll
-                for (int o = 1; o < J::CPR; o <<= 1)
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                float undo;
-                const float f = range_scale(mx, &undo);
-                if (undo != 1.f) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        x1[e] *= f;
-                        if constexpr (kHalf) x2[e] *= f;
-                    }
-                }
-                if (q == 0) bar.q_scale[(t + x) * kBM + r] = undo;
-                uint8_t *low = smem + Tc<D>::kOffQLo + (t + x) * Tc<D>::kTile;
-                uint4 lo;
-                *reinterpret_cast<uint4 *>(tile + oa) = half_parts(x1, b.precise, &lo);
-                if (b.precise) *reinterpret_cast<uint4 *>(low + oa) = lo;
-                if constexpr (kHalf) {
-                    *reinterpret_cast<uint4 *>(tile + ob) = half_parts(x2, b.precise, &lo);
-                    if (b.precise) *reinterpret_cast<uint4 *>(low + ob) = lo;
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < J::PPJ; ++e) {
-                const float nc = fmaf(c[e], sc[e], -s[e] * ss[e]);
-                s[e] = fmaf(c[e], ss[e], s[e] * sc[e]);
-                c[e] = nc;
-            }
+            const float nc = fmaf(c[e], sc[e], -s[e] * ss[e]);
+            s[e] = fmaf(c[e], ss[e], s[e] * sc[e]);
+            c[e] = nc;
         }
     }
 }
@@ -668,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         mbar_init(&bar.full_q, 1);
-        mbar_init(&bar.ready_q, 128);
+        mbar_init(&bar.ready_q, 384);
         for (int s = 0; s < NS; ++s) {
             mbar_init(&bar.full_k[s], 1);
             mbar_init(&bar.empty_k[s], 1);
@@ -804,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 acc || kk > 0);
             };
             uint32_t cleaned = 0, landed = 0;             // next parity of clean_v, full_v
-            bool ok = mbar_wait(&bar.ready_q, 0, abort, tmo);
+            bool ok = mbar_wait(p.fp16 ? &bar.ready_q : &bar.full_q, 0, abort, tmo);
             if (ok) ok = mbar_wait(&bar.full_k[0], 0, abort, tmo);
             if (ok) {
                 tc_fence_after();
@@ -852,14 +858,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         if (B.n > 0) {
             if (p.fp16) {
-                rotate_queries<D, kHalf>(p, B, tw, smem, bar, abort, tmo, ok);
                 wait_previous_kernel();
-                if (ok && keys_scaled(p, B, tw)) bar.k_scaled = 1;
-            } else {
-                ok = __all_sync(0xffffffffu, mbar_wait(&bar.full_q, 0, abort, tmo));
-            }
-            if (ok) {
-                fence_proxy_async_smem();
+                if (keys_scaled(p, B, tw)) bar.k_scaled = 1;
                 mbar_arrive(&bar.ready_q);
             }
             int nb = 0;
@@ -885,6 +885,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         setmaxnreg_inc<kRegsSoftmax>();
         // ------------------------------------------------ softmax of tile t
         const int t = warp >> 2, row = (warp & 3) * 32 + lane;
+        bool ok = true;
+        if (p.fp16 && B.n > 0) {
+            rotate_queries<D, kHalf>(p, B, threadIdx.x, smem, bar, abort, tmo, ok);
+            if (ok) {
+                fence_proxy_async_smem();
+                mbar_arrive(&bar.ready_q);
+            }
+        }
         if (t < B.nt) {
             const bool valid = row < B.rows(t);
             const int pos = B.pos(t) + row, h = B.h0 + t * B.hstep;
@@ -892,10 +900,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t trow = tmem + (uint32_t((warp & 3) * 32) << 16);
             const uint32_t s_col = t * kBN, o_col = C::kColO + t * D;
             float m = -INFINITY, l = 0.f, cl2 = v.c_log2;
-            bool ok = true, scaled = false;
-            if (B.n > 0) {
+            bool scaled = false;
+            if (p.fp16 && B.n > 0 && ok) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&bar.ready_q, 0, abort, tmo));
-                if (p.fp16) cl2 *= bar.q_scale[t * kBM + row];
+                cl2 *= bar.q_scale[t * kBM + row];
                 scaled = bar.k_scaled != 0;
             }
             for (int j = 0; ok && j < B.n; ++j) {
@@ -971,8 +979,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok) {
                 tc_fence_after();
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                __nv_bfloat16 *dst =
-                    reinterpret_cast<__nv_bfloat16 *>(v.o) + prow * v.os[0] + h * v.os[1];
+                // The rows go through the query tile's place (all its products are done)
+                // and out as whole rows: a warp's own 32, so only the warp waits.
+                uint8_t *stage = smem + t * C::kTile + row * (D * 2);
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     float o[32];
@@ -1006,15 +1015,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    if (valid) {
-                        uint4 *out = reinterpret_cast<uint4 *>(dst + c * 32);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            out[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]),
-                                                pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
-                                                pack_bf16x2(o[8 * e + 4], o[8 * e + 5]),
-                                                pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4 *>(stage + (((c * 4 + e) ^ (row & 7)) << 4)) =
+                            make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]),
+                                       pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                                       pack_bf16x2(o[8 * e + 4], o[8 * e + 5]),
+                                       pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+                }
+                __syncwarp();
+                constexpr int CR = D / 8, RI = 32 / CR;   // chunks of a row, rows at a time
+                const int w0 = (warp & 3) * 32, rows = B.rows(t);
+                const long long o0 = (long long)(B.u.q0 + t * B.rstep) * v.os[0] + h * v.os[1];
+#pragma unroll 4
+                for (int i = 0; i < 32; i += RI) {
+                    const int r = w0 + i + lane / CR, ch = lane % CR;
+                    const uint4 y = *reinterpret_cast<const uint4 *>(
+                        smem + t * C::kTile + r * (D * 2) + ((ch ^ (r & 7)) << 4));
+                    if (r < rows)
+                        *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(v.o) + o0 +
+                                                   r * v.os[0] + ch * 8) = y;
                 }
                 if (valid && v.lse)
                     v.lse[(long long)h * v.Tq + prow] =
@@ -1174,6 +1194,13 @@ lcx_status run_tc(const lcx_varlen_args *a, const VarlenParams &v, cudaStream_t 
         lo = k.lo;
         p.k_scale = k.scale;
         p.k_flags = k.flags;
+    }
+    if (rotate) {
+        const int cpr = half ? int(a->D / 16) : int(a->D / 8);
+        for (int i = 0; i < a->D / 2; ++i) {
+            const double ang = (256 / cpr) * v.theta[i];
+            p.step[i] = make_float2(float(std::cos(ang)), float(std::sin(ang)));
+        }
     }
     CUtensorMap m[4];
     lcx_status st;
