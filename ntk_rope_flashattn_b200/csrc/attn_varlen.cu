@@ -415,10 +415,11 @@ __global__ void __launch_bounds__(kKeyThreads)
 
 // ------------------------------------------------------------------ tcgen05 kernel
 constexpr int kThreads = 512, kBM = 128, kBN = 128;
+constexpr int kRotThreads = 384;    // warps 0-11 rotate the queries
 // registers a thread after the warpgroups re-balance: 176 + 176 + 96 + 64 = 4 x 128
 constexpr int kRegsSoftmax = 176, kRegsHelp = 96, kRegsIssue = 64;
 static_assert(2 * kRegsSoftmax + kRegsHelp + kRegsIssue == 4 * 128, "register file split");
-constexpr int kWarpHelp = 8, kWarpTma = 12, kWarpMma = 13, kWarpTmaV = 14;
+constexpr int kWarpHelp = 8, kWarpTma = 12, kWarpMma = 13, kWarpTmaV = 14, kWarpFlags = 15;
 constexpr float kLazy = 15.f;       // log2 growth of a row's maximum that rescales O
 constexpr int kMaxBorder = 8;       // border tiles whose non-finite rows are listed
 
@@ -460,7 +461,12 @@ struct Bars {
     int abort, k_scaled, n_border, any_bad;
     int border_tile[kMaxBorder];
     uint32_t bad[kMaxBorder][4];    // rows of a border tile with non-finite values
-    float q_scale[2 * kBM];
+    signed char q_exp[2 * kBM];     // exponents of the query rows' scales
+    // per pair, for the query rotation (lanes read different entries, which the
+    // parameter space would serve one after the other): the angle of the block's first
+    // position reduced to [-pi, pi], theta in two fp32 parts, cos and sin of the step
+    float base[64];
+    float2 theta[64], step[64];
 };
 
 // A CTA's work: the row block, its two tiles and the key tiles it visits.
@@ -526,6 +532,11 @@ __device__ __forceinline__ uint32_t chunk_off(int r, int fc) {
     return (fc >> 3) * (128 * 128) + r * 128 + (((fc & 7) ^ (r & 7)) << 4);
 }
 
+// The lowest n bits (n <= 0: none, n >= 32: all).
+__device__ __forceinline__ uint32_t below(int n) {
+    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1;
+}
+
 // Max of 128 values, four chains of 3-input maxima.
 __device__ __forceinline__ float row_max(const float (&v)[128]) {
     float m0 = v[0], m1 = v[1], m2 = v[2], m3 = v[3];
@@ -541,80 +552,128 @@ __device__ __forceinline__ float row_max(const float (&v)[128]) {
     return fmaxf(max3(m0, m1, m2), m3);
 }
 
-// The query tiles rotated in shared memory by the 256 softmax threads: bf16 -> fp16
-// parts (and, precise, remainders), one scale per row.  A thread handles the pairs
-// of one job in every RP-th row; two tiles of the same rows share the angles, which
-// step by RP positions (at most 15 steps of 2^-23 each).
+// The query tiles rotated in shared memory by the softmax and helper threads (384):
+// bf16 -> fp16 parts (and, precise, remainders), one power of two per row.  A thread
+// handles the pairs of one job in every RP-th row; two tiles of the same rows share
+// the angles, which step by RP positions (at most 15 steps of 2^-23 each), and are
+// worked on together: a warp has only its own independent work to hide latency with.
 template <int D, bool kHalf>
-__device__ __forceinline__ void rotate_queries(const TcParams &p, const Block &b, int tid,
-                                               uint8_t *smem, Bars<Tc<D>::NS> &bar,
-                                               volatile int *abort, uint64_t tmo, bool &ok) {
+__device__ __forceinline__ void rotate_queries(const Block &b, int tid, uint8_t *smem,
+                                               Bars<Tc<D>::NS> &bar, volatile int *abort,
+                                               uint64_t tmo, bool &ok) {
     using J = Job<D, kHalf>;
-    constexpr int RP = 256 / J::CPR;
+    constexpr int RP = kRotThreads / J::CPR;
     const int q = tid % J::CPR, r0 = tid / J::CPR;
-    const bool two_blocks = b.rstep != 0 && b.nt == 2;
-    const int rows = two_blocks ? 2 * kBM : kBM, both = two_blocks ? 1 : b.nt;
-    float c[J::PPJ], s[J::PPJ], sc[J::PPJ], ss[J::PPJ];
+    const bool two_blocks = b.rstep != 0 && b.nt == 2, pair = !two_blocks && b.nt == 2;
+    const int rows = two_blocks ? 2 * kBM : kBM;
+    float c[J::PPJ], s[J::PPJ];
+    float2 st[J::PPJ];
 #pragma unroll
     for (int e = 0; e < J::PPJ; ++e) {
-        __sincosf(rope_reduced_angle((long long)b.u.pos0 + r0, p.v.theta[q * J::PPJ + e]), &s[e],
-                  &c[e]);
-        sc[e] = p.step[q * J::PPJ + e].x;
-        ss[e] = p.step[q * J::PPJ + e].y;
+        // The row's angle r0 theta (r0 < 96) on top of the block's: 2 pi in two parts, the
+        // first of 16 bits so that its multiples are exact; within 2^-22 in all.  (The
+        // fp64 reduction per thread took 2.3k cycles of the 384 threads.)
+        const float2 th = bar.theta[q * J::PPJ + e];
+        const float r = static_cast<float>(r0);
+        const float k = rintf(r * th.x * 0.15915494f);
+        float a = fmaf(r, th.x, -k * 6.28314208984375f);
+        a = fmaf(k, -4.32173358e-5f, a);
+        a = fmaf(r, th.y, a) + bar.base[q * J::PPJ + e];
+        const float k2 = rintf(a * 0.15915494f);
+        a = fmaf(k2, -4.32173358e-5f, fmaf(k2, -6.28314208984375f, a));
+        __sincosf(a, &s[e], &c[e]);
+        st[e] = bar.step[q * J::PPJ + e];
     }
     ok = __all_sync(0xffffffffu, mbar_wait(&bar.full_q, 0, abort, tmo));
     if (!ok) return;
 #pragma unroll 1
-    for (int R = r0; R < rows; R += RP) {
-        const int r = R & (kBM - 1), t0 = R >> 7;
-#pragma unroll 1
-        for (int x = 0; x < both; ++x) {
-            uint8_t *tile = smem + (t0 + x) * Tc<D>::kTile;
+    for (int R0 = 0; R0 < rows; R0 += RP) {
+        const int R = R0 + r0;
+        if (R < rows) {
+            const int r = R & (kBM - 1), t0 = R >> 7;
             const uint32_t oa = chunk_off(r, q), ob = chunk_off(r, q + D / 16);
-            float x1[8], x2[8];
-            unpack(*reinterpret_cast<const uint4 *>(tile + oa), x1);
-            if constexpr (kHalf) unpack(*reinterpret_cast<const uint4 *>(tile + ob), x2);
-            turn<kHalf>(x1, x2, c, s);
-            float mx = kHalf ? fmaxf(abs_max8(x1), abs_max8(x2)) : abs_max8(x1);
+            uint8_t *tile = smem + t0 * Tc<D>::kTile;
+            float x1[2][8], x2[2][8];
+            uint4 va[2], vb[2];
 #pragma unroll
-            for (int o = 1; o < J::CPR; o <<= 1)
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            float undo;
-            const float f = range_scale(mx, &undo);
-            if (undo != 1.f) {
+            for (int x = 0; x < 2; ++x) {
+                // (one tile: the second copy is computed and not stored)
+                uint8_t *from = tile + (pair ? x : 0) * Tc<D>::kTile;
+                va[x] = *reinterpret_cast<const uint4 *>(from + oa);
+                if constexpr (kHalf) vb[x] = *reinterpret_cast<const uint4 *>(from + ob);
+            }
+            float mx[2];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x1[e] *= f;
-                    if constexpr (kHalf) x2[e] *= f;
+            for (int x = 0; x < 2; ++x) {
+                unpack(va[x], x1[x]);
+                if constexpr (kHalf) unpack(vb[x], x2[x]);
+                turn<kHalf>(x1[x], x2[x], c, s);
+                mx[x] = kHalf ? fmaxf(abs_max8(x1[x]), abs_max8(x2[x])) : abs_max8(x1[x]);
+            }
+            int ex[2] = {0, 0};
+            // (rows, and the rows of a pass, are whole warps': the warp is together here)
+            // without a value out of range in any lane no row maximum is needed
+            constexpr uint32_t lanes = 0xffffffffu;
+            const bool in = mx[0] >= 0.015625f && mx[0] < 16384.f && mx[1] >= 0.015625f &&
+                            mx[1] < 16384.f;
+            if (__any_sync(lanes, !in)) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                    for (int o = 1; o < J::CPR; o <<= 1)
+                        mx[x] = fmaxf(mx[x], __shfl_xor_sync(lanes, mx[x], o));
+                    float undo;
+                    const float f = range_scale(mx[x], &undo);
+                    ex[x] = int(__float_as_uint(undo) >> 23) - 127;
+                    if (ex[x]) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            x1[x][e] *= f;
+                            if constexpr (kHalf) x2[x][e] *= f;
+                        }
+                    }
                 }
             }
-            if (q == 0) bar.q_scale[(t0 + x) * kBM + r] = undo;
-            uint8_t *low = smem + Tc<D>::kOffQLo + (t0 + x) * Tc<D>::kTile;
-            const uint4 h1 = half_parts(x1);
-            *reinterpret_cast<uint4 *>(tile + oa) = h1;
-            if (b.precise) *reinterpret_cast<uint4 *>(low + oa) = half_rest(x1, h1);
-            if constexpr (kHalf) {
-                const uint4 h2 = half_parts(x2);
-                *reinterpret_cast<uint4 *>(tile + ob) = h2;
-                if (b.precise) *reinterpret_cast<uint4 *>(low + ob) = half_rest(x2, h2);
-            }
-        }
 #pragma unroll
-        for (int e = 0; e < J::PPJ; ++e) {
-            const float nc = fmaf(c[e], sc[e], -s[e] * ss[e]);
-            s[e] = fmaf(c[e], ss[e], s[e] * sc[e]);
-            c[e] = nc;
+            for (int x = 0; x < 2; ++x) {
+                if (x == 1 && !pair) break;
+                uint8_t *to = tile + x * Tc<D>::kTile;
+                uint8_t *low = to + Tc<D>::kOffQLo;
+                if (q == 0) bar.q_exp[(t0 + x) * kBM + r] = (signed char)ex[x];
+                const uint4 h1 = half_parts(x1[x]);
+                *reinterpret_cast<uint4 *>(to + oa) = h1;
+                if (b.precise) *reinterpret_cast<uint4 *>(low + oa) = half_rest(x1[x], h1);
+                if constexpr (kHalf) {
+                    const uint4 h2 = half_parts(x2[x]);
+                    *reinterpret_cast<uint4 *>(to + ob) = h2;
+                    if (b.precise) *reinterpret_cast<uint4 *>(low + ob) = half_rest(x2[x], h2);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < J::PPJ; ++e) {
+                const float nc = fmaf(c[e], st[e].x, -s[e] * st[e].y);
+                s[e] = fmaf(c[e], st[e].y, s[e] * st[e].x);
+                c[e] = nc;
+            }
         }
     }
 }
 
-// Whether any key of the block's sequence is scaled.
-__device__ __forceinline__ bool keys_scaled(const TcParams &p, const Block &b, int tw) {
+// Whether any key of the block's sequence is scaled (a warp; every lane a part).
+__device__ __forceinline__ bool keys_scaled(const TcParams &p, const Block &b, int lane) {
     if (!p.k_scale || b.u.nk == 0) return false;
     const int f0 = b.u.k0 / p.flag_rows, f1 = (b.u.k0 + b.u.nk - 1) / p.flag_rows;
     bool any = false;
-    for (int f = f0 + tw; f <= f1; f += 128) any |= p.k_flags[f] != 0;
+#pragma unroll 8
+    for (int f = f0 + lane; f <= f1; f += 32) any |= p.k_flags[f] != 0;
     return any;
+}
+
+// 32 bytes to global memory (32-byte aligned).
+__device__ __forceinline__ void store32(void *dst, const uint4 &a, const uint4 &b) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x),
+                 "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
 }
 
 // Helper thread tw cleans row tw of a border tile's values: a row behind the
@@ -672,9 +731,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     // K and V stages in use: precise blocks keep the keys' parts in two K stages
     const int mask = B.precise ? 0 : NS - 1, shift = B.precise ? 0 : (NS == 4 ? 2 : 1);
 
-    if (threadIdx.x == 0) {
+    // The query's way is the longest: its copies go out before anything else.
+    if (warp == kWarpTma && lane == 0) {
         mbar_init(&bar.full_q, 1);
-        mbar_init(&bar.ready_q, 384);
+        fence_mbar_init();
+        if (B.u.rows > 0 && B.n > 0 && !p.stall) {
+            mbar_arrive_expect_tx(&bar.full_q, B.nt * C::kTile);
+            for (int t = 0; t < B.nt; ++t)
+                for (int x = 0; x < D / 64; ++x)
+                    tma_load_4d(smem + t * C::kTile + x * C::kBox, &tmq, &bar.full_q, x * 64,
+                                B.u.q0 + t * B.rstep, B.h0 + t * B.hstep, 0);
+        }
+    }
+    if (p.fp16 && threadIdx.x >= 128 && threadIdx.x < 128 + D / 2) {
+        const int i = threadIdx.x - 128;
+        const double th = v.theta[i];
+        const float hi = static_cast<float>(th);
+        bar.base[i] = rope_reduced_angle((long long)B.u.pos0, th);
+        bar.theta[i] = make_float2(hi, static_cast<float>(th - hi));
+        bar.step[i] = p.step[i];
+    }
+    if (threadIdx.x == 0) {
+        mbar_init(&bar.ready_q, kRotThreads + 1);
         for (int s = 0; s < NS; ++s) {
             mbar_init(&bar.full_k[s], 1);
             mbar_init(&bar.empty_k[s], 1);
@@ -718,13 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         setmaxnreg_dec<kRegsIssue>();
         if (warp == kWarpTma && lane == 0 && B.n > 0 && !p.stall) {
             // ------------------------------------------------ Q and K producer
-            tma_prefetch_desc(&tmq);
             tma_prefetch_desc(&tmk);
-            mbar_arrive_expect_tx(&bar.full_q, B.nt * C::kTile);
-            for (int t = 0; t < B.nt; ++t)
-                for (int x = 0; x < D / 64; ++x)
-                    tma_load_4d(smem + t * C::kTile + x * C::kBox, &tmq, &bar.full_q, x * 64,
-                                B.u.q0 + t * B.rstep, B.h0 + t * B.hstep, 0);
             wait_previous_kernel();                       // the rotated keys
             uint32_t used = 0;                            // stages with a copy issued
             bool ok = true;
@@ -773,6 +845,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (used >> s & 1) mbar_wait(&bar.full_v[s], (phase >> s & 1) ^ 1, nullptr, tmo);
                 if (used_b >> s & 1)
                     mbar_wait(&bar.full_b[s], (phase_b >> s & 1) ^ 1, nullptr, tmo);
+            }
+        } else if (warp == kWarpFlags && B.n > 0 && p.fp16) {
+            // ------------------------------------------------ are there scaled keys?
+            wait_previous_kernel();
+            const bool any = __any_sync(0xffffffffu, keys_scaled(p, B, lane));
+            if (lane == 0) {
+                bar.k_scaled = any;
+                mbar_arrive(&bar.ready_q);
             }
         } else if (warp == kWarpMma && lane == 0 && B.n > 0) {
             // ------------------------------------------------ MMA issuer
@@ -831,6 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     if (!ok) break;
                     issue_pv(t, s, j > 0);
+                    if (jn == B.n) mma_commit(&bar.o_ready[t]);
                     if (jn < B.n) {
                         if (t == 0) {
                             ok = mbar_wait(&bar.full_k[jn & mask], (jn >> shift) & 1, abort, tmo);
@@ -845,8 +926,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (jn < B.n) mma_commit(&bar.empty_k[jn & mask]);
                 }
             }
-            if (ok)
-                for (int t = 0; t < B.nt; ++t) mma_commit(&bar.o_ready[t]);
             // all issued products complete before TMEM is released
             mma_commit(&bar.drain);
             mbar_wait(&bar.drain, 0, nullptr, tmo);
@@ -858,9 +937,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         if (B.n > 0) {
             if (p.fp16) {
-                wait_previous_kernel();
-                if (keys_scaled(p, B, tw)) bar.k_scaled = 1;
-                mbar_arrive(&bar.ready_q);
+                rotate_queries<D, kHalf>(B, threadIdx.x, smem, bar, abort, tmo, ok);
+                if (ok) {
+                    fence_proxy_async_smem();
+                    mbar_arrive(&bar.ready_q);
+                }
             }
             int nb = 0;
             uint32_t phase = 0;
@@ -887,7 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = warp >> 2, row = (warp & 3) * 32 + lane;
         bool ok = true;
         if (p.fp16 && B.n > 0) {
-            rotate_queries<D, kHalf>(p, B, threadIdx.x, smem, bar, abort, tmo, ok);
+            rotate_queries<D, kHalf>(B, threadIdx.x, smem, bar, abort, tmo, ok);
             if (ok) {
                 fence_proxy_async_smem();
                 mbar_arrive(&bar.ready_q);
@@ -903,7 +984,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool scaled = false;
             if (p.fp16 && B.n > 0 && ok) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&bar.ready_q, 0, abort, tmo));
-                cl2 *= bar.q_scale[t * kBM + row];
+                cl2 *= __uint_as_float(uint32_t(127 + bar.q_exp[t * kBM + row]) << 23);
                 scaled = bar.k_scaled != 0;
             }
             for (int j = 0; ok && j < B.n; ++j) {
@@ -921,14 +1002,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (e < last) x[e] *= ks[(long long)e * v.Hkv];
                 }
                 if (!tile_full(v, B, t, jt)) {
-                    // visible: e <= hi and (no window or e >= lo or e < sk)
+                    // visible: e <= hi and (no window or e >= lo or e < sk), a bit per
+                    // key in four words
                     const int hi = v.causal ? min(pos - k0, B.u.nk - 1 - k0) : B.u.nk - 1 - k0;
-                    const int lo = pos - v.window + 1 - k0, sk = v.sinks - k0;
-                    const bool win = v.window > 0;
+                    const int lo = v.window > 0 ? pos - v.window + 1 - k0 : 0, sk = v.sinks - k0;
 #pragma unroll
-                    for (int e = 0; e < kBN; ++e) {
-                        const bool keep = (e <= hi) & (!win | (e >= lo) | (e < sk));
-                        x[e] = keep ? x[e] : -INFINITY;
+                    for (int g = 0; g < kBN / 32; ++g) {
+                        const uint32_t keep =
+                            below(hi + 1 - 32 * g) & (~below(lo - 32 * g) | below(sk - 32 * g));
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            x[32 * g + e] = (keep >> e) & 1 ? x[32 * g + e] : -INFINITY;
                     }
                 }
                 const float m_new = fmaxf(m, row_max(x) * cl2);
@@ -982,6 +1066,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // The rows go through the query tile's place (all its products are done)
                 // and out as whole rows: a warp's own 32, so only the warp waits.
                 uint8_t *stage = smem + t * C::kTile + row * (D * 2);
+                const bool wide =
+                    !((reinterpret_cast<uintptr_t>(v.o) | (v.os[0] * 2) | (v.os[1] * 2)) & 31);
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     float o[32];
@@ -1024,17 +1110,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
                 }
                 __syncwarp();
-                constexpr int CR = D / 8, RI = 32 / CR;   // chunks of a row, rows at a time
                 const int w0 = (warp & 3) * 32, rows = B.rows(t);
-                const long long o0 = (long long)(B.u.q0 + t * B.rstep) * v.os[0] + h * v.os[1];
+                __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(v.o) +
+                                     (long long)(B.u.q0 + t * B.rstep) * v.os[0] + h * v.os[1];
+                auto piece = [&](int r, int ch) {
+                    return *reinterpret_cast<const uint4 *>(smem + t * C::kTile + r * (D * 2) +
+                                                            ((ch ^ (r & 7)) << 4));
+                };
+                if (wide) {
+                    constexpr int CR = D / 16, RI = 32 / CR;   // 32-byte pieces of a row
+#pragma unroll
+                    for (int i = 0; i < 32; i += RI) {
+                        const int r = w0 + i + lane / CR, ch = lane % CR;
+                        const uint4 y0 = piece(r, 2 * ch), y1 = piece(r, 2 * ch + 1);
+                        if (r < rows) store32(out + r * v.os[0] + ch * 16, y0, y1);
+                    }
+                } else {
+                    constexpr int CR = D / 8, RI = 32 / CR;    // 16-byte pieces
 #pragma unroll 4
-                for (int i = 0; i < 32; i += RI) {
-                    const int r = w0 + i + lane / CR, ch = lane % CR;
-                    const uint4 y = *reinterpret_cast<const uint4 *>(
-                        smem + t * C::kTile + r * (D * 2) + ((ch ^ (r & 7)) << 4));
-                    if (r < rows)
-                        *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(v.o) + o0 +
-                                                   r * v.os[0] + ch * 8) = y;
+                    for (int i = 0; i < 32; i += RI) {
+                        const int r = w0 + i + lane / CR, ch = lane % CR;
+                        const uint4 y = piece(r, ch);
+                        if (r < rows) *reinterpret_cast<uint4 *>(out + r * v.os[0] + ch * 8) = y;
+                    }
                 }
                 if (valid && v.lse)
                     v.lse[(long long)h * v.Tq + prow] =
@@ -1198,7 +1296,7 @@ lcx_status run_tc(const lcx_varlen_args *a, const VarlenParams &v, cudaStream_t 
     if (rotate) {
         const int cpr = half ? int(a->D / 16) : int(a->D / 8);
         for (int i = 0; i < a->D / 2; ++i) {
-            const double ang = (256 / cpr) * v.theta[i];
+            const double ang = (kRotThreads / cpr) * v.theta[i];
             p.step[i] = make_float2(float(std::cos(ang)), float(std::sin(ang)));
         }
     }
