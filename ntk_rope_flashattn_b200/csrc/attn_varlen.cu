@@ -50,16 +50,20 @@ namespace lcx {
 namespace {
 
 // ------------------------------------------------------------------ fp32 kernel
-// 64 query rows of one head per CTA, key tiles of 64, all products in fp32 on
-// the FMA pipe.  Thread (ty, tx) of 16 x 16 owns rows 4 ty .. 4 ty + 3, the scores
-// of keys tx + 16 j, and output columns 4 tx + 64 c.
+// 64 query rows of one head per CTA, key tiles of 64, all products in fp32 on the FMA
+// pipe, which bounds it (128 lanes per SM).  Thread (ty, tx) of 16 x 16 owns rows
+// 4 ty .. 4 ty + 3, the scores of keys tx + 16 j, and output columns 4 tx + 64 c;
+// every operand is read four wide from shared memory (12 wavefronts per 64 products
+// a warp, below the pipe's 16 cycles).  P takes the place of the key tile, so that two
+// CTAs (D = 128) or four (D = 64) share an SM and one's loads overlap another's products.
 constexpr int kRows = 64, kKeys = 64, kSimtThreads = 256;
 
 template <int D>
 struct Simt {
     static constexpr int LD = D + 4;      // padded row of a Q or K tile (floats)
-    static constexpr int LP = kKeys + 4;  // padded row of the P tile
-    static constexpr int kFloats = kRows * LD + kKeys * LD + kKeys * D + kRows * LP;
+    static constexpr int LP = kKeys + 4;  // padded row of the P tile (in the K tile's place)
+    static constexpr int kFloats = kRows * LD + kKeys * LD + kKeys * D;
+    static_assert(LP <= LD, "P in the place of K");
     static constexpr int kBytes = kFloats * 4;
 };
 
@@ -78,11 +82,11 @@ __device__ __forceinline__ void load4(const T *src, float (&x)[4]) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kSimtThreads)
+__global__ void __launch_bounds__(kSimtThreads, 2)
     varlen_simt_kernel(const __grid_constant__ VarlenParams p) {
     using C = Simt<D>;
     extern __shared__ float sm[];
-    float *sq = sm, *sk = sq + kRows * C::LD, *sv = sk + kKeys * C::LD, *sp = sv + kKeys * D;
+    float *sq = sm, *sk = sq + kRows * C::LD, *sv = sk + kKeys * C::LD, *sp = sk;
     const int h = blockIdx.x % p.Hq, uu = blockIdx.x / p.Hq;
     const VarlenUnit U = load_unit(p, uu >> 1);
     const int r0 = (uu & 1) * kRows, rows = min(kRows, U.rows - r0);
@@ -119,6 +123,7 @@ __global__ void __launch_bounds__(kSimtThreads)
     for (int j0 = 0; j0 < jhi; j0 += kKeys) {
         if (j0 + kKeys <= jlo && j0 >= p.sinks) continue;
         __syncthreads();
+        bool bad = false;               // some value of the tile is not finite
         for (int i = threadIdx.x; i < kKeys * (D / 4); i += kSimtThreads) {
             const int r = i / (D / 4), c = i % (D / 4) * 4;
             float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
@@ -126,11 +131,14 @@ __global__ void __launch_bounds__(kSimtThreads)
                 const long long row = U.k0 + j0 + r;
                 load4(reinterpret_cast<const T *>(p.k) + row * p.ks[0] + g * p.ks[1] + c, x);
                 load4(reinterpret_cast<const T *>(p.v) + row * p.vs[0] + g * p.vs[1] + c, y);
+                // 0 x: zero, or NaN for an infinite or NaN value
+                const float z = 0.f * y[0] + 0.f * y[1] + 0.f * y[2] + 0.f * y[3];
+                bad |= z != 0.f;
             }
             *reinterpret_cast<float4 *>(sk + r * C::LD + c) = make_float4(x[0], x[1], x[2], x[3]);
             *reinterpret_cast<float4 *>(sv + r * D + c) = make_float4(y[0], y[1], y[2], y[3]);
         }
-        __syncthreads();
+        bad = __syncthreads_or(bad);
         float s[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -155,6 +163,7 @@ __global__ void __launch_bounds__(kSimtThreads)
                     s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
                 }
         }
+        __syncthreads();                // every score is computed: P may replace the keys
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int pos = pos0 + 4 * ty + i;
@@ -177,8 +186,9 @@ __global__ void __launch_bounds__(kSimtThreads)
             for (int j = 0; j < 4; ++j) {
                 const float w = s[i][j] == -INFINITY ? 0.f : exp2f(s[i][j] - mn);
                 z += w;
-                // hidden weights are marked so that the product skips the value
-                sp[(4 * ty + i) * C::LP + tx + 16 * j] = seen[j] ? w : -1.f;
+                // (with non-finite values about, hidden weights are marked so that the
+                // product skips them)
+                sp[(4 * ty + i) * C::LP + tx + 16 * j] = seen[j] || !bad ? w : -1.f;
             }
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o, 16);
@@ -189,22 +199,28 @@ __global__ void __launch_bounds__(kSimtThreads)
         }
         __syncthreads();
 #pragma unroll 2
-        for (int j = 0; j < kKeys; ++j) {
-            float w[4];
+        for (int j = 0; j < kKeys; j += 4) {
+            float w[4][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = sp[(4 * ty + i) * C::LP + j];
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                const float4 v = *reinterpret_cast<const float4 *>(sv + j * D + 64 * c + 4 * tx);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (w[i] == -1.f) continue;
-                    acc[i][4 * c] = fmaf(w[i], v.x, acc[i][4 * c]);
-                    acc[i][4 * c + 1] = fmaf(w[i], v.y, acc[i][4 * c + 1]);
-                    acc[i][4 * c + 2] = fmaf(w[i], v.z, acc[i][4 * c + 2]);
-                    acc[i][4 * c + 3] = fmaf(w[i], v.w, acc[i][4 * c + 3]);
-                }
+            for (int i = 0; i < 4; ++i) {
+                const float4 y = *reinterpret_cast<const float4 *>(sp + (4 * ty + i) * C::LP + j);
+                w[i][0] = y.x; w[i][1] = y.y; w[i][2] = y.z; w[i][3] = y.w;
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    const float4 v =
+                        *reinterpret_cast<const float4 *>(sv + (j + k) * D + 64 * c + 4 * tx);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (bad && w[i][k] == -1.f) continue;
+                        acc[i][4 * c] = fmaf(w[i][k], v.x, acc[i][4 * c]);
+                        acc[i][4 * c + 1] = fmaf(w[i][k], v.y, acc[i][4 * c + 1]);
+                        acc[i][4 * c + 2] = fmaf(w[i][k], v.z, acc[i][4 * c + 2]);
+                        acc[i][4 * c + 3] = fmaf(w[i][k], v.w, acc[i][4 * c + 3]);
+                    }
+                }
         }
     }
 #pragma unroll

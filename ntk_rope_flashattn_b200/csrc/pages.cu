@@ -14,14 +14,14 @@
 namespace lcx {
 namespace {
 
-constexpr int kT = 1024;  // threads of a deciding CTA: one entry each
+constexpr int kT = 1024;  // threads of a deciding CTA, at most: one entry each
 static_assert(kT == LCX_PAGES_MAX_ENTRIES, "one thread per entry");
 
-// Inclusive prefix sum of x over the CTA's kT threads; *total = the whole sum.
-// Safe to call repeatedly.
+// Inclusive prefix sum of x over the CTA's threads; *total = the whole sum.  Safe to
+// call repeatedly.
 __device__ int block_scan(int x, int *total) {
     __shared__ int warp_sum[kT / 32];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x / 32;
     int v = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -31,7 +31,7 @@ __device__ int block_scan(int x, int *total) {
     if (lane == 31) warp_sum[w] = v;
     __syncthreads();
     if (w == 0) {
-        int s = warp_sum[lane];
+        int s = lane < warps ? warp_sum[lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, s, o);
@@ -41,7 +41,7 @@ __device__ int block_scan(int x, int *total) {
     }
     __syncthreads();
     v += w > 0 ? warp_sum[w - 1] : 0;
-    *total = warp_sum[kT / 32 - 1];
+    *total = warp_sum[warps - 1];
     __syncthreads();
     return v;
 }
@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(kT)
     __syncthreads();
     // Every page taken by its own thread: page t of the block belongs to the
     // first entry whose running end lies beyond t.
-    for (int t = i; t < taken; t += kT) {
-        int lo = 0, hi = kT - 1;
+    for (int t = i; t < taken; t += blockDim.x) {
+        int lo = 0, hi = int(blockDim.x) - 1;
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (s_end[mid] > t) hi = mid; else lo = mid + 1;
@@ -124,19 +124,24 @@ __global__ void __launch_bounds__(kT)
 __global__ void __launch_bounds__(kT)
     fork_kernel(const __grid_constant__ PagedParams p, const int *src, const int *dst, int n,
                 int *status) {
-    __shared__ int s_dst[kT];
+    __shared__ int s_dst[kT], s_free[kT];
     const PagedScratch x = paged_scratch(p.scratch, p.P);
     const int i = threadIdx.x;
     const int a = i < n ? src[i] : -1, b = i < n ? dst[i] : -1;
     s_dst[i] = b;
-    __syncthreads();
+    // (loads that need not wait for one another go out together: the kernel's time is
+    // a chain of them)
     const int avail = free_depth(p);
+    const bool named = a >= 0 && b >= 0, in = named && a < p.S && b < p.S;
+    const int len_a = in ? p.lens[a] : 0, len_b = in ? p.lens[b] : 0;
+    if (i < avail) s_free[i] = p.free_pages[avail - 1 - i];
+    __syncthreads();
     int len = -1, need = 0, old_page = -1;
-    if (a >= 0 && b >= 0) {
-        if (a >= p.S || b >= p.S || p.lens[b] != 0 || seen_before(s_dst, i, b)) {
+    if (named) {
+        if (!in || len_b != 0 || seen_before(s_dst, i, b)) {
             raise_status(status, LCX_ERR_INVALID_ARG);
         } else {
-            len = p.lens[a];
+            len = len_a;
             if (len < 0 || len > (long long)p.MP * p.ps) {
                 raise_status(status, LCX_ERR_INVALID_ARG);
                 len = -1;
@@ -158,8 +163,8 @@ __global__ void __launch_bounds__(kT)
     const int taken = min(total, avail);
     int page = -1;
     if (granted && need) {
-        const int at = avail - taken + incl - 1;
-        page = p.free_pages[at];
+        const int at = avail - taken + incl - 1;   // taken <= n: among the staged ones
+        page = s_free[avail - 1 - at];
         p.free_pages[at] = -1;
         if (page < 0 || page >= p.P) {
             raise_status(status, LCX_ERR_INVALID_ARG);
@@ -198,6 +203,7 @@ __device__ __forceinline__ long long page_vec(const PageShape &g, bool dense, in
 }
 
 constexpr int kCopyThreads = 256, kCopyVecs = 4;  // a CTA step copies 16 KB
+constexpr int kCopyCtas = 8;                      // CTAs per SM
 
 // Copy the n_pairs page pairs of the scratch list, every layer, K and V.
 __device__ void copy_pairs(const PagedParams &p, const PageShape &g, const PagedScratch &x) {
@@ -454,6 +460,9 @@ lcx_status entries_ok(const void *a, const void *b, int64_t n, const char *what)
     return LCX_OK;
 }
 
+// Threads of a CTA that decides about n entries (more than n take pages in extend).
+unsigned deciding(int64_t n) { return unsigned(std::max<int64_t>(256, (n + 31) / 32 * 32)); }
+
 lcx_status launched(cudaError_t e, const char *what) {
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess)
@@ -550,7 +559,7 @@ extern "C" lcx_status lcx_pages_extend(const lcx_paged_cache *cache, const int32
     lcx_status st = paged_prepare(cache, p);
     if (st != LCX_OK) return st;
     if ((st = entries_ok(seq_ids, start, n, "extend")) != LCX_OK || n == 0) return st;
-    extend_kernel<<<1, kT, 0, static_cast<cudaStream_t>(stream)>>>(p, seq_ids, n_new, int(n),
+    extend_kernel<<<1, deciding(n), 0, static_cast<cudaStream_t>(stream)>>>(p, seq_ids, n_new, int(n),
                                                                    start, dev_status);
     return launched(cudaSuccess, "pages_extend");
 }
@@ -564,9 +573,9 @@ extern "C" lcx_status lcx_pages_fork(const lcx_paged_cache *cache, const int32_t
     if (st != LCX_OK) return st;
     if ((st = entries_ok(src, dst, n, "fork")) != LCX_OK || n == 0) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    fork_kernel<<<1, kT, 0, s>>>(p, src, dst, int(n), dev_status);
+    fork_kernel<<<1, deciding(n), 0, s>>>(p, src, dst, int(n), dev_status);
     if ((st = launched(cudaSuccess, "pages_fork")) != LCX_OK) return st;
-    return launched(launch_dependent(fork_apply_kernel, dim3(device_sms() * 4),
+    return launched(launch_dependent(fork_apply_kernel, dim3(device_sms() * kCopyCtas),
                                      dim3(kCopyThreads), 0, s, p, page_shape(p), src, dst, int(n),
                                      dev_status),
                     "pages_fork");
@@ -581,7 +590,7 @@ extern "C" lcx_status lcx_pages_free(const lcx_paged_cache *cache, const int32_t
     if ((st = entries_ok(seq_ids, seq_ids, n, "free")) != LCX_OK || n == 0) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const long long warps = n * ((p.MP + 31) / 32);
-    const unsigned grid = unsigned(std::min<long long>((warps + 7) / 8, device_sms() * 4));
+    const unsigned grid = unsigned(std::min<long long>((warps + 7) / 8, device_sms() * kCopyCtas));
     release_kernel<<<grid, 256, 0, s>>>(p, seq_ids, int(n), dev_status);
     if ((st = launched(cudaSuccess, "pages_free")) != LCX_OK) return st;
     return launched(launch_dependent(collect_kernel, dim3(1), dim3(kT), 0, s, p, seq_ids, int(n),
@@ -598,7 +607,7 @@ extern "C" lcx_status lcx_pages_compact(const lcx_paged_cache *cache, int32_t *d
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     compact_kernel<<<1, kT, 0, s>>>(p);
     if ((st = launched(cudaSuccess, "pages_compact")) != LCX_OK) return st;
-    return launched(launch_dependent(compact_apply_kernel, dim3(device_sms() * 4),
+    return launched(launch_dependent(compact_apply_kernel, dim3(device_sms() * kCopyCtas),
                                      dim3(kCopyThreads), 0, s, p, page_shape(p), dev_status),
                     "pages_compact");
 }
@@ -612,9 +621,9 @@ extern "C" lcx_status lcx_pages_copy(const lcx_paged_cache *cache, const int32_t
     if (st != LCX_OK) return st;
     if ((st = entries_ok(src_pages, dst_pages, n, "copy")) != LCX_OK || n == 0) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    copy_list_kernel<<<1, kT, 0, s>>>(p, src_pages, dst_pages, int(n), dev_status);
+    copy_list_kernel<<<1, deciding(n), 0, s>>>(p, src_pages, dst_pages, int(n), dev_status);
     if ((st = launched(cudaSuccess, "pages_copy")) != LCX_OK) return st;
-    return launched(launch_dependent(copy_kernel, dim3(device_sms() * 4), dim3(kCopyThreads), 0, s,
+    return launched(launch_dependent(copy_kernel, dim3(device_sms() * kCopyCtas), dim3(kCopyThreads), 0, s,
                                      p, page_shape(p)),
                     "pages_copy");
 }
