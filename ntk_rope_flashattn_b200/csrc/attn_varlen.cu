@@ -108,13 +108,14 @@ __global__ void __launch_bounds__(kSimtThreads, 2)
         sq[r * C::LD + a] = x * c - y * s;
         sq[r * C::LD + b] = x * s + y * c;
     }
-    float m[4], l[4], acc[4][D / 16];
+    float m[4], l[4];
+    float2 acc[4][D / 32];              // columns 64 c + 4 tx + {0, 1}, {2, 3}
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
+        for (int c = 0; c < D / 32; ++c) acc[i][c] = make_float2(0.f, 0.f);
     }
     // keys any row of the tile sees: [0, jhi), without (sinks .. jlo) under a window
     const int last = pos0 + rows - 1;
@@ -139,11 +140,12 @@ __global__ void __launch_bounds__(kSimtThreads, 2)
             *reinterpret_cast<float4 *>(sv + r * D + c) = make_float4(y[0], y[1], y[2], y[3]);
         }
         bad = __syncthreads_or(bad);
-        float s[4][4];
+        // even and odd columns summed apart, two products an instruction
+        float2 s2[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+            for (int j = 0; j < 4; ++j) s2[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
         for (int d = 0; d < D; d += 4) {
             float4 a[4], b[4];
@@ -157,12 +159,17 @@ __global__ void __launch_bounds__(kSimtThreads, 2)
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
-                    s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
-                    s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
-                    s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+                    s2[i][j] = fma2(make_float2(a[i].x, a[i].y), make_float2(b[j].x, b[j].y),
+                                    s2[i][j]);
+                    s2[i][j] = fma2(make_float2(a[i].z, a[i].w), make_float2(b[j].z, b[j].w),
+                                    s2[i][j]);
                 }
         }
+        float s[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = s2[i][j].x + s2[i][j].y;
         __syncthreads();                // every score is computed: P may replace the keys
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -195,7 +202,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2)
             m[i] = mn;
             l[i] = l[i] * al + z;
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) acc[i][c] *= al;
+            for (int c = 0; c < D / 32; ++c) acc[i][c] = mul2(acc[i][c], make_float2(al, al));
         }
         __syncthreads();
 #pragma unroll 2
@@ -215,10 +222,9 @@ __global__ void __launch_bounds__(kSimtThreads, 2)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         if (bad && w[i][k] == -1.f) continue;
-                        acc[i][4 * c] = fmaf(w[i][k], v.x, acc[i][4 * c]);
-                        acc[i][4 * c + 1] = fmaf(w[i][k], v.y, acc[i][4 * c + 1]);
-                        acc[i][4 * c + 2] = fmaf(w[i][k], v.z, acc[i][4 * c + 2]);
-                        acc[i][4 * c + 3] = fmaf(w[i][k], v.w, acc[i][4 * c + 3]);
+                        const float2 w2 = make_float2(w[i][k], w[i][k]);
+                        acc[i][2 * c] = fma2(w2, make_float2(v.x, v.y), acc[i][2 * c]);
+                        acc[i][2 * c + 1] = fma2(w2, make_float2(v.z, v.w), acc[i][2 * c + 1]);
                     }
                 }
         }
@@ -232,10 +238,12 @@ __global__ void __launch_bounds__(kSimtThreads, 2)
         const long long row = U.q0 + r0 + r;
         T *dst = reinterpret_cast<T *>(p.o) + row * p.os[0] + h * p.os[1];
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
+        for (int c = 0; c < D / 64; ++c) {
+            const float2 x = acc[i][2 * c], y = acc[i][2 * c + 1];
+            const float o[4] = {x.x * inv, x.y * inv, y.x * inv, y.y * inv};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                dst[64 * c + 4 * tx + e] = static_cast<T>(acc[i][4 * c + e] * inv);
+            for (int e = 0; e < 4; ++e) dst[64 * c + 4 * tx + e] = static_cast<T>(o[e]);
+        }
         if (p.lse && tx == 0)
             p.lse[(long long)h * p.Tq + row] =
                 l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718055994531f;
