@@ -164,15 +164,18 @@ def _index(cache, **tensors):
     return out
 
 
-def _launch(cache, call, *args):
-    """call(*args, stream) with the cache's device current, on its current stream."""
+def _call_on(dev, call, *args):
+    """call(*args, stream) with device `dev` current, on its current stream."""
     import torch
-    dev = cache.device.index
     if torch.cuda.current_device() == dev:
         _check(call(*args, torch.cuda.current_stream(dev).cuda_stream))
     else:
         with torch.cuda.device(dev):
             _check(call(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
+def _launch(cache, call, *args):
+    _call_on(cache.device.index, call, *args)
 
 
 def pages_extend(cache, seq_ids, n_new=None, start=None, status=None):
@@ -274,30 +277,31 @@ def paged_append(cache, k, v, seq_ids, start, rope: RopeParams, layer: int = 0, 
     if cu_new is None and T != seq_ids.shape[0]:
         raise ValueError("without cu_new k must have one row per entry")
     ids, st, cu, word = _index(cache, seq_ids=seq_ids, start=start, cu_new=cu_new, status=status)
-    a = _AppendArgs()
-    a.k, a.v, a.k_strides, a.v_strides = k.data_ptr(), v.data_ptr(), _strides3(k), _strides3(v)
+    Hq = 0
     if q is not None:
         _tokens(q, "q", None, D, cache.dtype)
         if q.shape[0] != T:
             raise ValueError("q must have k's %d rows" % T)
         if q_out is None:
             q_out = torch.empty_like(q)
-        _tokens(q_out, "q_out", q.shape[1], D, cache.dtype)
+        Hq = q.shape[1]
+        _tokens(q_out, "q_out", Hq, D, cache.dtype)
         if q_out.shape != q.shape:
             raise ValueError("q_out must be shaped like q")
-        a.q, a.q_out, a.Hq = q.data_ptr(), q_out.data_ptr(), q.shape[1]
-        a.q_strides, a.q_out_strides = _strides3(q), _strides3(q_out)
     elif q_out is not None:
         raise ValueError("q_out without q")
     if k_out is not None:
         _tokens(k_out, "k_out", H, D, cache.dtype)
         if k_out.shape != k.shape:
             raise ValueError("k_out must be shaped like k")
-        a.k_out, a.k_out_strides = k_out.data_ptr(), _strides3(k_out)
-    a.seq_ids, a.start, a.cu_new, a.dev_status = ids, st, cu, word
-    a.n, a.T, a.layer = seq_ids.numel(), T, int(layer)
-    rope_c = _rope_c(rope)
-    a.rope = rope_c
+    none = _Strides3()
+    rope_c = _rope_c(rope)      # (alive during the call: it owns factor tables)
+    a = _AppendArgs(
+        k.data_ptr(), v.data_ptr(), None if q is None else q.data_ptr(),
+        None if q is None else q_out.data_ptr(), None if k_out is None else k_out.data_ptr(), ids,
+        st, cu, word, seq_ids.shape[0], T, Hq, int(layer), _strides3(k), _strides3(v),
+        none if q is None else _strides3(q), none if q is None else _strides3(q_out),
+        none if k_out is None else _strides3(k_out), rope_c)
     _launch(cache, load().lcx_paged_append, cache._struct, ctypes.byref(a))
     return q_out
 
@@ -347,8 +351,9 @@ def paged_decode(cache, q, seq_ids, rope: RopeParams, layer: int = 0, window: in
     if workspace is None and Hq % cache.kv_heads == 0:
         need = paged_decode_workspace_bytes(cache, n, Hq)
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+    rope_c = _rope_c(rope)      # (alive during the call: it owns factor tables)
     a = _DecodeArgs(q.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(), ids, word,
-                    n, Hq, int(layer), _strides3(q), _strides3(o), _rope_c(rope), int(window),
+                    n, Hq, int(layer), _strides3(q), _strides3(o), rope_c, int(window),
                     int(sinks), float(softmax_scale), LCX_DECODE_PREROTATED if prerotated else 0)
     ws, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
     _launch(cache, load().lcx_paged_decode, cache._struct, ctypes.byref(a), ws, size)

@@ -9,7 +9,7 @@ import ctypes
 import numpy as np
 
 from . import RopeParams, _check, _dtype_code, _RopeParams, _same_device, load
-from .paged import _rope_c, _strides3
+from .paged import _call_on, _rope_c, _strides3
 
 LCX_VARLEN_PREROTATED = 1
 LCX_VARLEN_TEST_STALL = 0x80000000
@@ -72,14 +72,8 @@ class VarlenPlan:
         _check(load().lcx_varlen_plan(pq, pk, n, host.data_ptr(), ints, ctypes.byref(self.info)))
         self.device = device
         self.plan = host.to(device)
-
-    @property
-    def total_q(self) -> int:
-        return int(self.info.total_q)
-
-    @property
-    def total_k(self) -> int:
-        return int(self.info.total_k)
+        self.total_q, self.total_k = int(self.info.total_q), int(self.info.total_k)
+        self._workspace_bytes = {}
 
     @property
     def cu_q(self):
@@ -96,13 +90,16 @@ class VarlenPlan:
 
 def varlen_workspace_bytes(plan: VarlenPlan, kv_heads: int, head_dim: int, dtype) -> int:
     """Workspace bytes of ``attn_varlen`` (lcx_varlen_workspace_bytes)."""
-    import torch
-    code = {torch.bfloat16: 0, torch.float32: 1}.get(dtype, -1)
-    need = int(load().lcx_varlen_workspace_bytes(ctypes.byref(plan.info), int(kv_heads),
-                                                 int(head_dim), code))
-    if need < 0:
-        raise ValueError("attn_varlen: %s kv heads, head_dim %s, %s are not supported" %
-                         (kv_heads, head_dim, dtype))
+    need = plan._workspace_bytes.get((kv_heads, head_dim, dtype))
+    if need is None:
+        import torch
+        code = {torch.bfloat16: 0, torch.float32: 1}.get(dtype, -1)
+        need = int(load().lcx_varlen_workspace_bytes(ctypes.byref(plan.info), int(kv_heads),
+                                                     int(head_dim), code))
+        if need < 0:
+            raise ValueError("attn_varlen: %s kv heads, head_dim %s, %s are not supported" %
+                             (kv_heads, head_dim, dtype))
+        plan._workspace_bytes[(kv_heads, head_dim, dtype)] = need
     return need
 
 
@@ -124,18 +121,17 @@ def attn_varlen(q, k, v, plan: VarlenPlan, rope: RopeParams, causal: bool = True
     share one).  A query without a visible key gets
     o = 0 and lse = -inf.  ``status`` and ``watchdog_ms`` as for ``attn_fwd``."""
     import torch
-    for t in (q, k, v):
-        if t.dim() != 3 or not t.is_cuda:
-            raise ValueError("q, k, v must be 3-D CUDA tensors [tokens, heads, D]")
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or not (q.is_cuda and k.is_cuda and v.is_cuda):
+        raise ValueError("q, k, v must be 3-D CUDA tensors [tokens, heads, D]")
     Tq, Hq, D = q.shape
-    Tk, Hkv = k.shape[0], k.shape[1]
-    if k.shape != (Tk, Hkv, D) or v.shape != k.shape:
+    Tk, Hkv, Dk = k.shape
+    if Dk != D or v.shape != k.shape:
         raise ValueError("shape mismatch: q %s k %s v %s" % (q.shape, k.shape, v.shape))
     if not (q.dtype == k.dtype == v.dtype):
         raise ValueError("q, k, v must share a dtype")
-    _same_device(q, k=k, v=v, out=out, lse=lse, workspace=workspace, status=status, plan=plan.plan)
-    whole = plan.total_q == Tq
-    alloc = torch.empty if whole else torch.zeros
+    _same_device(q, k=k, v=v, out=out, lse=lse, workspace=workspace, status=status,
+                 plan=plan.plan)
+    alloc = torch.empty if plan.total_q == Tq else torch.zeros
     o = out if out is not None else alloc((Tq, Hq, D), dtype=q.dtype, device=q.device)
     if o.shape != q.shape or o.dtype != q.dtype:
         raise ValueError("out must be shaped like q")
@@ -146,26 +142,18 @@ def attn_varlen(q, k, v, plan: VarlenPlan, rope: RopeParams, causal: bool = True
         raise ValueError("lse must be contiguous fp32 [%d, %d]" % (Hq, Tq))
     if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
         raise ValueError("status must be an int32 tensor")
-    a = _VarlenArgs()
-    a.q, a.k, a.v, a.o = q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr()
-    a.lse = None if lse is None else lse.data_ptr()
-    a.plan, a.info = plan.plan.data_ptr(), plan.info
-    a.dev_status = None if status is None else status.data_ptr()
-    if not prerotated and rope.mode != "none" and workspace is None:
+    if workspace is None and not prerotated and rope.mode != "none":
         workspace = torch.empty(max(varlen_workspace_bytes(plan, Hkv, D, k.dtype), 1),
                                 dtype=torch.uint8, device=k.device)
-    if workspace is not None:
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.nbytes
-    a.dtype, a.causal = _dtype_code(q), 1 if causal else 0
-    a.Tq, a.Tk, a.Hq, a.Hkv, a.D = Tq, Tk, Hq, Hkv, D
-    a.q_strides, a.k_strides = _strides3(q), _strides3(k)
-    a.v_strides, a.o_strides = _strides3(v), _strides3(o)
-    rope_c = _rope_c(rope)
-    a.rope = rope_c
-    a.window, a.sinks, a.softmax_scale = int(window), int(sinks), float(softmax_scale)
-    a.flags = ((LCX_VARLEN_PREROTATED if prerotated else 0) |
-               (LCX_VARLEN_TEST_STALL if _test_stall else 0))
-    a.watchdog_ms = int(watchdog_ms)
-    with torch.cuda.device(q.device):
-        _check(load().lcx_attn_varlen(ctypes.byref(a), torch.cuda.current_stream().cuda_stream))
+    ws, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    rope_c = _rope_c(rope)      # (alive during the call: it owns factor tables)
+    a = _VarlenArgs(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+        None if lse is None else lse.data_ptr(), plan.plan.data_ptr(), ws, size,
+        None if status is None else status.data_ptr(), plan.info, _dtype_code(q),
+        1 if causal else 0, Tq, Tk, Hq, Hkv, D, _strides3(q), _strides3(k), _strides3(v),
+        _strides3(o), rope_c, int(window), int(sinks), float(softmax_scale),
+        (LCX_VARLEN_PREROTATED if prerotated else 0) |
+        (LCX_VARLEN_TEST_STALL if _test_stall else 0), int(watchdog_ms), 0)
+    _call_on(q.device.index, load().lcx_attn_varlen, ctypes.byref(a))
     return (o, lse) if return_lse else o

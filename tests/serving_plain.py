@@ -24,7 +24,8 @@ def table64(rope):
     import oracle
     t, ms = oracle.rope_theta_ext(rope.mode, rope.head_dim, rope.base, rope.scale,
                                   rope.original_max_pos, rope.alpha, rope.beta,
-                                  seq_len=rope.seq_len)
+                                  seq_len=rope.seq_len, factors=rope.factors,
+                                  factors_short=rope.factors_short)
     return torch.from_numpy(t).double(), float(ms)
 
 

@@ -138,6 +138,25 @@ def test_decode_modes_and_prerotated(mode, pairing):
                  torch.float32, 3, 400, "prerotated")
 
 
+def test_factor_tables_through_append_and_decode():
+    """Per-pair factors (host tables, built anew for every call): the long table beyond
+    the training length, the short one within it."""
+    import numpy as np
+    f, short = np.linspace(1.0, 7.0, 32), np.linspace(1.0, 1.5, 32)
+    for seq_len in (100, 3000):
+        rope = lcx.RopeParams("factors", 64, original_max_pos=1000, factors=f, factors_short=short,
+                              seq_len=seq_len)
+        lens = [40]
+        c, rows = cache_of(lens, 16, 2, 64, torch.float32)
+        k, v, q = (randn(i, 1, h, 64, dtype=torch.float32) for i, h in ((1, 2), (2, 2), (3, 4)))
+        start = lcx.pages_extend(c, ints([0]))
+        lcx.paged_append(c, k, v, ints([0]), start, rope)
+        kr = rotate(k.cpu(), torch.tensor([40]), rope)
+        rows = [(torch.cat([rows[0][0], kr]), torch.cat([rows[0][1], v.double().cpu()]))]
+        o, lse = lcx.paged_decode(c, q, ints([0]), rope, return_lse=True)
+        check_decode(o, lse, plain_decode(q, rows, [41], [0], rope), torch.float32, 2, 41)
+
+
 def test_decode_strided_tensors_and_layers():
     lens = [150, 20]
     rope = lcx.RopeParams("plain", 128)
