@@ -455,7 +455,8 @@ struct TcParams {
     const int *k_flags;             // per CTA of the key rotation
     int flag_rows;                  // tokens of such a CTA
     int mode, fp16;                 // fp16: rotated operands; 0: bf16 inputs as they are
-    int head_units;                 // CTAs per row block
+    int group_units;                // CTAs per row block and kv head
+    int by_head;                    // order of the CTAs (load_block)
     int stall;                      // the producers issue nothing (watchdog test hook)
     float2 step[64];                // cos, sin of the angle between a thread's rows
 };
@@ -477,8 +478,41 @@ struct Tc {
     static_assert(kColO + 2 * D <= 512, "TMEM budget");
 };
 
-template <int NS>
+
+// The key tiles that rows at positions i0 .. i1 see whole: [0, sf) (sinks) and
+// [jl, je).  The others that they visit are border tiles.
+struct Full {
+    int sf, jl, je;
+    __device__ __forceinline__ void set(const VarlenParams &v, int i0, int i1, int nk) {
+        const int lim = v.causal ? min(nk - 1, i0) : nk - 1;     // last key all rows see
+        je = lim < 0 ? 0 : (lim + 1) / kBN;
+        jl = 0;
+        sf = 0;
+        if (v.window > 0) {
+            jl = max(0, i1 - v.window + 1 + kBN - 1) / kBN;
+            sf = min(v.sinks / kBN, je);
+        }
+    }
+    __device__ __forceinline__ bool has(int jt) const { return jt < sf || (jt >= jl && jt < je); }
+};
+
+// A CTA's work: the row block, its two tiles and the key tiles it visits.
+struct Block {
+    VarlenUnit u;
+    int g, h0, nt, hstep, rstep;    // tile t: head h0 + t hstep, rows from t rstep on
+    int ns, jlo, n;                 // key tiles: sink tiles [0, ns), then from jlo on
+    Full full;                      // key tiles that every row of the block sees whole
+    bool precise;
+    __device__ __forceinline__ int tile(int j) const { return j < ns ? j : jlo + (j - ns); }
+    __device__ __forceinline__ int pos(int t) const { return u.pos0 + t * rstep; }
+    __device__ __forceinline__ int rows(int t) const { return min(kBM, u.rows - t * rstep); }
+};
+
+template <int D>
 struct Bars {
+    static constexpr int NS = Tc<D>::NS;
+    Block block;
+    Full own[2];                    // tiles that a query tile's own rows see whole
     uint64_t full_q, ready_q, full_k[NS], empty_k[NS], full_v[NS], full_b[NS], clean_v[NS], empty_v[NS];
     uint64_t s_ready[2], p_ready[2], o_ready[2], helped, drain;
     uint32_t tmem_base;
@@ -489,40 +523,38 @@ struct Bars {
     // per pair, for the query rotation (lanes read different entries, which the
     // parameter space would serve one after the other): the angle of the block's first
     // position reduced to [-pi, pi], theta in two fp32 parts, cos and sin of the step
-    float base[64];
-    float2 theta[64], step[64];
-};
-
-// A CTA's work: the row block, its two tiles and the key tiles it visits.
-struct Block {
-    VarlenUnit u;
-    int g, h0, nt, hstep, rstep;    // tile t: head h0 + t hstep, rows from t rstep on
-    int ns, jlo, n;                 // key tiles: sink tiles [0, ns), then from jlo on
-    bool precise;
-    __device__ __forceinline__ int tile(int j) const { return j < ns ? j : jlo + (j - ns); }
-    __device__ __forceinline__ int pos(int t) const { return u.pos0 + t * rstep; }
-    __device__ __forceinline__ int rows(int t) const { return min(kBM, u.rows - t * rstep); }
+    float base[D / 2];
+    float2 theta[D / 2], step[D / 2];
 };
 
 __device__ __forceinline__ Block load_block(const TcParams &p) {
     Block b;
     const VarlenParams &v = p.v;
-    const int hu = int(blockIdx.x) % p.head_units;
-    b.u = load_unit(v, int(blockIdx.x) / p.head_units);
+    const int per = v.n_units * p.group_units, all = p.group_units * v.Hkv;
+    int g, r;
+    if (p.by_head) {            // kv head, row block (heaviest first), the group's heads
+        g = int(blockIdx.x) / per;
+        r = int(blockIdx.x) % per;
+        b.u = load_unit(v, r / p.group_units);
+    } else {                    // row block, kv head, the group's heads
+        r = int(blockIdx.x) % all;
+        g = r / p.group_units;
+        b.u = load_unit(v, int(blockIdx.x) / all);
+    }
+    b.g = g;
     b.hstep = b.rstep = 0;
     b.nt = 1;
     if (p.mode == kTwoHeads) {
-        b.h0 = 2 * hu;
+        b.h0 = g * v.G + 2 * (r % p.group_units);
         b.nt = 2;
         b.hstep = 1;
     } else {
-        b.h0 = hu;
+        b.h0 = g * v.G + r % p.group_units;
         if (p.mode == kTwoBlocks) {
             b.rstep = kBM;
             b.nt = b.u.rows > kBM ? 2 : 1;
         }
     }
-    b.g = b.h0 / v.G;
     const int pa = b.u.pos0, pb = b.u.pos0 + b.u.rows - 1, nk = b.u.nk;
     const int last = v.causal ? min(pb, nk - 1) : nk - 1;     // last visible key
     b.jlo = 0;
@@ -532,23 +564,9 @@ __device__ __forceinline__ Block load_block(const TcParams &p) {
         b.ns = min((v.sinks + kBN - 1) / kBN, b.jlo);
     }
     b.n = last < 0 ? 0 : b.ns + (last / kBN - b.jlo + 1);
+    b.full.set(v, pa, pa + b.rstep * (b.nt - 1) + kBM - 1, nk);
     b.precise = p.fp16 && ((v.causal && pa < 127) || (v.window > 0 && v.window < 128) || nk < 128);
     return b;
-}
-
-// Every row of tile t sees every key of key tile jt.
-__device__ __forceinline__ bool tile_full(const VarlenParams &v, const Block &b, int t, int jt) {
-    const int j0 = jt * kBN, j1 = j0 + kBN - 1;
-    const int i0 = b.pos(t), i1 = i0 + kBM - 1;
-    if (j1 > b.u.nk - 1) return false;
-    if (!v.causal) return true;
-    if (j1 > i0) return false;
-    return v.window <= 0 || j0 >= i1 - v.window + 1 || j1 < v.sinks;
-}
-__device__ __forceinline__ bool is_border(const VarlenParams &v, const Block &b, int jt) {
-    for (int t = 0; t < b.nt; ++t)
-        if (!tile_full(v, b, t, jt)) return true;
-    return false;
 }
 
 // 16-byte chunk fc (8 columns) of row r in a tile of 128-byte swizzled boxes.
@@ -583,7 +601,7 @@ __device__ __forceinline__ float row_max(const float (&v)[128]) {
 // worked on together: a warp has only its own independent work to hide latency with.
 template <int D, bool kHalf>
 __device__ __forceinline__ void rotate_queries(const Block &b, int tid, uint8_t *smem,
-                                               Bars<Tc<D>::NS> &bar, volatile int *abort,
+                                               Bars<D> &bar, volatile int *abort,
                                                uint64_t tmo, bool &ok) {
     using J = Job<D, kHalf>;
     constexpr int RP = kRotThreads / J::CPR;
@@ -693,6 +711,25 @@ __device__ __forceinline__ bool keys_scaled(const TcParams &p, const Block &b, i
     return any;
 }
 
+// Multiply a row's scores of key tile jt (TMEM, from taddr on) by the keys' scales.
+__device__ __noinline__ void scale_scores(const TcParams &p, const Block &b, uint32_t taddr,
+                                          int jt) {
+    const int last = b.u.nk - jt * kBN;
+    const float *ks = p.k_scale + (long long)(b.u.k0 + jt * kBN) * p.v.Hkv + b.g;
+#pragma unroll 1
+    for (int c = 0; c < kBN; c += 32) {
+        float x[32];
+        tmem_ld32(taddr + c, x);
+        uint32_t u[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            const float f = c + e < last ? ks[(long long)(c + e) * p.v.Hkv] : 1.f;
+            u[e] = __float_as_uint(x[e] * f);
+        }
+        tmem_st32(taddr + c, u);
+    }
+}
+
 // 32 bytes to global memory (32-byte aligned).
 __device__ __forceinline__ void store32(void *dst, const uint4 &a, const uint4 &b) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x),
@@ -745,33 +782,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sK = smem + C::kOffK, *sV = smem + C::kOffV;
-    static_assert(sizeof(Bars<NS>) <= 2048, "barrier block");
-    Bars<NS> &bar = *reinterpret_cast<Bars<NS> *>(smem + C::kOffBar);
+    static_assert(sizeof(Bars<D>) <= 2048, "barrier block");
+    Bars<D> &bar = *reinterpret_cast<Bars<D> *>(smem + C::kOffBar);
     const VarlenParams &v = p.v;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int *abort = &bar.abort;
     const uint64_t tmo = v.timeout_ns;
-    const Block B = load_block(p);
-    // K and V stages in use: precise blocks keep the keys' parts in two K stages
-    const int mask = B.precise ? 0 : NS - 1, shift = B.precise ? 0 : (NS == 4 ? 2 : 1);
+    // (the block lives in shared memory: the roles keep of it what their loops need)
+    const Block &B = bar.block;
+    const Block b0 = load_block(p);
 
     // The query's way is the longest: its copies go out before anything else.
     if (warp == kWarpTma && lane == 0) {
         mbar_init(&bar.full_q, 1);
         fence_mbar_init();
-        if (B.u.rows > 0 && B.n > 0 && !p.stall) {
-            mbar_arrive_expect_tx(&bar.full_q, B.nt * C::kTile);
-            for (int t = 0; t < B.nt; ++t)
+        if (b0.u.rows > 0 && b0.n > 0 && !p.stall) {
+            mbar_arrive_expect_tx(&bar.full_q, b0.nt * C::kTile);
+            for (int t = 0; t < b0.nt; ++t)
                 for (int x = 0; x < D / 64; ++x)
                     tma_load_4d(smem + t * C::kTile + x * C::kBox, &tmq, &bar.full_q, x * 64,
-                                B.u.q0 + t * B.rstep, B.h0 + t * B.hstep, 0);
+                                b0.u.q0 + t * b0.rstep, b0.h0 + t * b0.hstep, 0);
         }
     }
     if (p.fp16 && threadIdx.x >= 128 && threadIdx.x < 128 + D / 2) {
         const int i = threadIdx.x - 128;
         const double th = v.theta[i];
         const float hi = static_cast<float>(th);
-        bar.base[i] = rope_reduced_angle((long long)B.u.pos0, th);
+        bar.base[i] = rope_reduced_angle((long long)b0.u.pos0, th);
         bar.theta[i] = make_float2(hi, static_cast<float>(th - hi));
         bar.step[i] = p.step[i];
     }
@@ -792,6 +829,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&bar.helped, 128);
         mbar_init(&bar.drain, 1);
+        bar.block = b0;
+        for (int t = 0; t < 2; ++t) bar.own[t].set(v, b0.pos(t), b0.pos(t) + kBM - 1, b0.u.nk);
         bar.abort = 0;
         bar.k_scaled = 0;
         bar.n_border = 0;
@@ -806,6 +845,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar.tmem_base;
+    // K and V stages in use: precise blocks keep the keys' parts in two K stages
+    const int mask = B.precise ? 0 : NS - 1, shift = B.precise ? 0 : (NS == 4 ? 2 : 1);
     bool pre = false;   // thread 0: an earlier CTA's wait ran out already
     if (threadIdx.x == 0 && v.status && *reinterpret_cast<volatile int *>(v.status) ==
                                             int(LCX_ERR_TIMEOUT)) {
@@ -856,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int s = j & mask;
                 if (j > mask) ok = mbar_wait(&bar.empty_v[s], ((j >> shift) - 1) & 1, abort, tmo);
                 if (!ok) break;
-                const bool border = is_border(v, B, B.tile(j));
+                const bool border = !B.full.has(B.tile(j));
                 uint64_t *full = border ? &bar.full_b[s] : &bar.full_v[s];
                 mbar_arrive_expect_tx(full, C::kTile);
                 for (int x = 0; x < D / 64; ++x)
@@ -880,33 +921,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == kWarpMma && lane == 0 && B.n > 0) {
             // ------------------------------------------------ MMA issuer
+            const int n = B.n, nt = B.nt, ns = B.ns, jlo = B.jlo;
+            const Full full = B.full;
+            const bool precise = B.precise;
             const uint32_t fmt = p.fp16 ? kFmtF16 : kFmtBF16;
             const uint32_t id_s = idesc_f32acc(128, kBN, 0, 0, 0, 0) | (fmt << 7) | (fmt << 10);
             constexpr uint32_t id_pv = idesc_bf16_f32(128, D, 0, 1);   // V as the TMA lands it
-            const uint64_t d0 = sdesc_sw128(smem_u32(smem), 16, 1024);
-            const uint32_t dhi = uint32_t(d0 >> 32), q_lo = uint32_t(d0);
-            const uint32_t k_lo = uint32_t(sdesc_sw128(smem_u32(sK), 16, 1024));
-            const uint32_t ql_lo = uint32_t(sdesc_sw128(smem_u32(smem + C::kOffQLo), 16, 1024));
-            const uint32_t v_lo = uint32_t(sdesc_sw128(smem_u32(sV), C::kBox, 1024));
-            auto product = [&](uint32_t dst, uint32_t qa, uint32_t ka, bool more) {
+            // Every operand's descriptor differs from the first query tile's by a
+            // constant: the start address, and for V (MN-major) the leading offset.
+            const uint32_t q_lo = uint32_t(sdesc_sw128(smem_u32(smem), 16, 1024));
+            constexpr uint32_t dhi = sdesc_hi_sw128(1024);
+            constexpr uint32_t kK = C::kOffK >> 4, kQLo = C::kOffQLo >> 4, kT = C::kTile >> 4;
+            constexpr uint32_t kV = (C::kOffV >> 4) + (((C::kBox >> 4) - 1) << 16);
+            auto product = [&](uint32_t dst, uint32_t qa, uint32_t ka, uint32_t more) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t o = ((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4;
-                    mma_ss_w<0>(dst, qa + o, ka + o, dhi, id_s, more || kk > 0);
+                    mma_ss_w<0>(dst, qa + o, ka + o, dhi, id_s, kk > 0 ? 1u : more);
                 }
             };
             auto issue_s = [&](int t, int s) {
-                const uint32_t dst = tmem + t * kBN, qa = q_lo + ((t * C::kTile) >> 4);
-                const uint32_t ka = k_lo + ((s * C::kTile) >> 4);
-                product(dst, qa, ka, false);
-                if (B.precise) {
-                    product(dst, qa, k_lo + (C::kTile >> 4), true);          // Qh Kl
-                    product(dst, ql_lo + ((t * C::kTile) >> 4), ka, true);   // Ql Kh
+                const uint32_t dst = tmem + t * kBN;
+                const uint32_t qa = q_lo + t * kT, ka = q_lo + kK + s * kT;
+                product(dst, qa, ka, 0);
+                if (precise) {
+                    // Qh Kl, then Ql Kh
+#pragma unroll 1
+                    for (int i = 0; i < 2; ++i)
+                        product(dst, i ? qa + kQLo : qa, i ? ka : q_lo + kK + kT, 1);
                 }
                 mma_commit(&bar.s_ready[t]);
             };
             auto issue_pv = [&](int t, int s, bool acc) {
-                const uint32_t va = v_lo + ((s * C::kTile) >> 4);
+                const uint32_t va = q_lo + kV + s * kT;
                 const uint32_t dst = tmem + C::kColO + t * D, pa = tmem + t * kBN;
 #pragma unroll
                 for (int kk = 0; kk < kBN / 16; ++kk)
@@ -918,25 +965,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok) ok = mbar_wait(&bar.full_k[0], 0, abort, tmo);
             if (ok) {
                 tc_fence_after();
-                for (int t = 0; t < B.nt; ++t) issue_s(t, 0);
+#pragma unroll 1
+                for (int t = 0; t < nt; ++t) issue_s(t, 0);
                 mma_commit(&bar.empty_k[0]);
             }
-            for (int j = 0; ok && j < B.n; ++j) {
+            for (int j = 0; ok && j < n; ++j) {
                 const int s = j & mask, jn = j + 1;
-                if (is_border(v, B, B.tile(j))) {
+                if (!full.has(j < ns ? j : jlo + (j - ns))) {
                     ok = mbar_wait(&bar.clean_v[s], (cleaned >> s) & 1, abort, tmo);
                     cleaned ^= 1u << s;
                 } else {
                     ok = mbar_wait(&bar.full_v[s], (landed >> s) & 1, abort, tmo);
                     landed ^= 1u << s;
                 }
-                for (int t = 0; ok && t < B.nt; ++t) {
+#pragma unroll 1
+                for (int t = 0; ok && t < nt; ++t) {
                     ok = mbar_wait(&bar.p_ready[t], j & 1, abort, tmo);
                     tc_fence_after();
                     if (!ok) break;
                     issue_pv(t, s, j > 0);
-                    if (jn == B.n) mma_commit(&bar.o_ready[t]);
-                    if (jn < B.n) {
+                    if (jn == n) mma_commit(&bar.o_ready[t]);
+                    if (jn < n) {
                         if (t == 0) {
                             ok = mbar_wait(&bar.full_k[jn & mask], (jn >> shift) & 1, abort, tmo);
                             tc_fence_after();
@@ -947,7 +996,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (ok) {
                     mma_commit(&bar.empty_v[s]);
-                    if (jn < B.n) mma_commit(&bar.empty_k[jn & mask]);
+                    if (jn < n) mma_commit(&bar.empty_k[jn & mask]);
                 }
             }
             // all issued products complete before TMEM is released
@@ -971,7 +1020,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t phase = 0;
             for (int j = 0; ok && j < B.n; ++j) {
                 const int jt = B.tile(j), s = j & mask;
-                if (!is_border(v, B, jt)) continue;
+                if (B.full.has(jt)) continue;
                 ok = __all_sync(0xffffffffu,
                                 mbar_wait(&bar.full_b[s], (phase >> s) & 1, abort, tmo));
                 phase ^= 1u << s;
@@ -999,36 +1048,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (t < B.nt) {
-            const bool valid = row < B.rows(t);
-            const int pos = B.pos(t) + row, h = B.h0 + t * B.hstep;
-            const long long prow = B.u.q0 + t * B.rstep + row;
+            // (a row of scores takes 128 of the 176 registers: what the key loop needs of
+            // the block is read again for every tile, while the scores are computed)
+            const int n = B.n;
             const uint32_t trow = tmem + (uint32_t((warp & 3) * 32) << 16);
             const uint32_t s_col = t * kBN, o_col = C::kColO + t * D;
             float m = -INFINITY, l = 0.f, cl2 = v.c_log2;
             bool scaled = false;
-            if (p.fp16 && B.n > 0 && ok) {
+            if (p.fp16 && n > 0 && ok) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&bar.ready_q, 0, abort, tmo));
                 cl2 *= __uint_as_float(uint32_t(127 + bar.q_exp[t * kBM + row]) << 23);
                 scaled = bar.k_scaled != 0;
             }
-            for (int j = 0; ok && j < B.n; ++j) {
+            for (int j = 0; ok && j < n; ++j) {
+                const int jt = B.tile(j);
+                const bool whole = bar.own[t].has(jt);
                 ok = __all_sync(0xffffffffu, mbar_wait(&bar.s_ready[t], j & 1, abort, tmo));
                 if (!ok) break;
                 tc_fence_after();
-                const int jt = B.tile(j), k0 = jt * kBN;
+                if (scaled) scale_scores(p, B, trow + s_col, jt);
                 float x[kBN];
                 tmem_ld128(trow + s_col, x);
-                if (scaled) {
-                    const float *ks = p.k_scale + (long long)(B.u.k0 + k0) * v.Hkv + B.g;
-                    const int last = min(kBN, B.u.nk - k0);
-#pragma unroll
-                    for (int e = 0; e < kBN; ++e)
-                        if (e < last) x[e] *= ks[(long long)e * v.Hkv];
-                }
-                if (!tile_full(v, B, t, jt)) {
+                if (!whole) {
                     // visible: e <= hi and (no window or e >= lo or e < sk), a bit per
                     // key in four words
-                    const int hi = v.causal ? min(pos - k0, B.u.nk - 1 - k0) : B.u.nk - 1 - k0;
+                    const int k0 = jt * kBN, nk = B.u.nk, pos = B.pos(t) + row;
+                    const int hi = v.causal ? min(pos - k0, nk - 1 - k0) : nk - 1 - k0;
                     const int lo = v.window > 0 ? pos - v.window + 1 - k0 : 0, sk = v.sinks - k0;
 #pragma unroll
                     for (int g = 0; g < kBN / 32; ++g) {
@@ -1078,7 +1123,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             bool bad = false;
             int nb = 0;
-            if (ok && B.n > 0) {
+            const bool valid = row < B.rows(t);
+            const int h = B.h0 + t * B.hstep, pos = B.pos(t) + row;
+            if (ok && n > 0) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&bar.o_ready[t], 0, abort, tmo)) &&
                      __all_sync(0xffffffffu, mbar_wait(&bar.helped, 0, abort, tmo));
                 bad = bar.any_bad != 0;
@@ -1095,7 +1142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     float o[32];
-                    if (B.n > 0) {
+                    if (n > 0) {
                         tmem_ld32(trow + o_col + c * 32, o);
                     } else {
 #pragma unroll
@@ -1159,7 +1206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (valid && v.lse)
-                    v.lse[(long long)h * v.Tq + prow] =
+                    v.lse[(long long)h * v.Tq + B.u.q0 + t * B.rstep + row] =
                         l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
             }
         }
@@ -1258,7 +1305,7 @@ lcx_status launch_tc(const CUtensorMap (&m)[4], TcParams &p, bool after_keys, cu
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<D>::kSmem);
     if (e != cudaSuccess)
         return fail(LCX_ERR_CUDA, "cudaFuncSetAttribute failed: %s", cudaGetErrorString(e));
-    const long long grid = (long long)p.v.n_units * p.head_units;
+    const long long grid = (long long)p.v.n_units * p.group_units * p.v.Hkv;
     if (grid > 0x7fffffffLL) return fail(LCX_ERR_UNSUPPORTED, "too many work units");
     if (after_keys)
         e = launch_dependent(kern, dim3(unsigned(grid)), dim3(kThreads), Tc<D>::kSmem, s, m[0],
@@ -1284,7 +1331,13 @@ lcx_status run_tc(const lcx_varlen_args *a, const VarlenParams &v, cudaStream_t 
     // row blocks runs faster over twice the CTAs, one tile each.
     const int64_t pairs = v.G % 2 == 0 ? I.n_units[0] * (v.Hq / 2) : I.n_units[1] * v.Hq;
     p.mode = pairs < device_sms() ? kOneTile : v.G % 2 == 0 ? kTwoHeads : kTwoBlocks;
-    p.head_units = p.mode == kTwoHeads ? v.Hq / 2 : v.Hq;
+    p.group_units = p.mode == kTwoHeads ? v.G / 2 : v.G;
+    // Order of the CTAs.  All heads of the heaviest row blocks first balances best;
+    // when the keys and values of all heads exceed what L2 holds for both dies, kv head
+    // by kv head reads them from there instead (15.8k tokens of 8 heads, 65 MB: 384
+    // against 401 us; 16.4k, 67 MB: the same; 26k, 107 MB: 2734 against 2626 us; 32.8k:
+    // 8955 against 8715 us).
+    p.by_head = I.total_k * v.Hkv * a->D * 4 > (int64_t(80) << 20);
     const int which = p.mode == kTwoBlocks;
     p.v.units =
         reinterpret_cast<const VarlenUnit *>(a->plan + plan_units(I.n_seqs, which, I.n_units[0]));

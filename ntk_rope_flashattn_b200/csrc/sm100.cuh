@@ -281,6 +281,11 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t smem_addr, uint32_t lbo
     return d;
 }
 
+// The upper word of such a descriptor (it does not depend on the address).
+__host__ __device__ constexpr uint32_t sdesc_hi_sw128(uint32_t sbo_bytes) {
+    return (sbo_bytes >> 4) | (1u << 14) | (2u << 29);
+}
+
 // Instruction descriptor with fp32 accumulation (D format 1 in bits 4-5), the A
 // and B formats in bits 7-9 and 10-12, MN-major flags in bits 15/16, N/8 in bits
 // 17-22 and M/16 in bits 24-28.  Formats: kind::f16 takes 0 = f16, 1 = bf16;
