@@ -154,6 +154,62 @@ def test_hidden_nan_and_infinity(Hq, H, D, dt):
         assert torch.equal(la[:, 200:], lb[:, 200:])     # values do not enter the lse
 
 
+MANY = [(37 * i * i + 11 * i) % 330 for i in range(48)] + [1, 0, 128, 256, 257, 511]
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (60, 0), (200, 70)])
+@pytest.mark.parametrize("Hq,H,D", [(8, 2, 128), (8, 2, 64), (9, 3, 128), (10, 2, 64), (6, 6, 64)])
+def test_many_sequences(Hq, H, D, window, sinks):
+    """Enough row blocks for two query tiles a CTA: two heads of an even group, two row
+    blocks of an odd one, precise blocks among them, chunks with keys before them."""
+    lk = [n + (7 * i) % 90 if i % 3 == 0 else n for i, n in enumerate(MANY)]
+    rope = lcx.RopeParams("yarn", D, scale=4.0, original_max_pos=64)
+    q, k, v = (randn(i, n, h, D) for i, n, h in ((1, sum(MANY), Hq), (2, sum(lk), H),
+                                                 (3, sum(lk), H)))
+    o, lse = lcx.attn_varlen(q, k, v, lcx.VarlenPlan(MANY, lk), rope, window=window, sinks=sinks,
+                             return_lse=True)
+    compare(o, lse, plain(q, k, v, MANY, lk, rope, True, window, sinks), torch.bfloat16, 511)
+    o2 = lcx.attn_varlen(q, k, v, lcx.VarlenPlan(MANY, lk), rope, window=window, sinks=sinks)
+    assert torch.equal(o, o2)
+
+
+@pytest.mark.parametrize("Hq,H,D", [(8, 2, 128), (9, 3, 64)])
+def test_many_sequences_hidden_values_and_scaled_keys(Hq, H, D):
+    """With two query tiles a CTA: a NaN and an infinite value in one late token of every
+    sequence, and keys far outside fp16's range."""
+    rope = lcx.RopeParams("plain", D)
+    plan = lcx.VarlenPlan(MANY)
+    T = sum(MANY)
+    q, k, v = (randn(i, T, h, D) for i, h in ((1, Hq), (2, H), (3, H)))
+    a, la = lcx.attn_varlen(q, k, v, plan, rope, return_lse=True)
+    v2, sees = v.clone(), torch.zeros(T, dtype=torch.bool, device="cuda")
+    at = 0
+    for i, n in enumerate(MANY):
+        if n > 1:
+            t = at + (3 * n) // 4
+            v2[t, i % H, 3] = float("nan")
+            v2[t, i % H, 5] = float("inf")
+            sees[t:at + n] = True
+        at += n
+    b, lb = lcx.attn_varlen(q, k, v2, plan, rope, return_lse=True)
+    hit = ~torch.isfinite(b.float())
+    assert torch.equal(la, lb) and not hit[~sees].any()
+    assert torch.equal(a[~hit], b[~hit])
+    assert not hit[:, :, [c for c in range(D) if c not in (3, 5)]].any()
+    G, at = Hq // H, 0
+    for i, n in enumerate(MANY):
+        if n > 1:
+            t, h = at + (3 * n) // 4, slice((i % H) * G, (i % H) * G + G)
+            assert torch.isnan(b[t:at + n, h, 3].float()).all()
+            assert (b[t:at + n, h, 5] == float("inf")).all()
+            assert int(hit[at:at + n].sum()) == 2 * G * (at + n - t)
+        at += n
+    ks, qs = k.clone(), (q.float() * 2.0 ** -20).bfloat16()
+    ks[::50] = (k[::50].float() * 2.0 ** 20).bfloat16()
+    o, lse = lcx.attn_varlen(qs, ks, v, plan, rope, return_lse=True)
+    compare(o, lse, plain(qs, ks, v, MANY, MANY, rope), torch.bfloat16, 511)
+
+
 def test_nan_value_of_one_column():
     """A NaN in one column of one visible value reaches that column of the queries
     that see it, and nothing else."""
