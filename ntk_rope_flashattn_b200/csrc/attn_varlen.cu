@@ -5,7 +5,7 @@
 // sequence ("Long Context: RoPE / YaRN / NTK / MLA", 2.4, 10.1, 10.2), with a
 // running maximum and sum ("8.3 长上下文技术", 8.3.4).
 //
-// bf16: the tcgen05 kernel below; fp32: a kernel of fp32 products behind it.
+// bf16: the tcgen05 kernel described here; fp32: the kernel of tf32 products below.
 //
 // The tcgen05 kernel is bound by the tensor core (4 D flops per visible pair and
 // query head) and, per key tile, by the softmax's 128 x 128 exponentials per query
@@ -40,6 +40,7 @@
 
 #include <cuda.h>
 
+#include "mma_sync.cuh"
 #include "paged.cuh"
 #include "rope_angle.cuh"
 #include "sm100.cuh"
@@ -50,217 +51,339 @@ namespace lcx {
 namespace {
 
 // ------------------------------------------------------------------ fp32 kernel
-// 64 query rows of one head per CTA, key tiles of 64, all products in fp32 on the FMA
-// pipe, which bounds it (128 lanes per SM).  Thread (ty, tx) of 16 x 16 owns rows
-// 4 ty .. 4 ty + 3, the scores of keys tx + 16 j, and output columns 4 tx + 64 c;
-// every operand is read four wide from shared memory (12 wavefronts per 64 products
-// a warp, below the pipe's 16 cycles).  P takes the place of the key tile, so that two
-// CTAs (D = 128) or four (D = 64) share an SM and one's loads overlap another's products.
-constexpr int kRows = 64, kKeys = 64, kSimtThreads = 256;
+// 64 query rows of one head per CTA, key tiles of 64, 8 warps: warp w has rows
+// 16 (w % 4) .. + 15 and, with half = w / 4, the scores of 32 keys and half of the
+// output's columns.  Both products are tf32 matrix instructions on two parts of every
+// operand, each part a cut of the value (hi + lo within 2^-21 of it): lo hi + hi lo +
+// hi hi, three instructions and still above the FMA pipe's rate (254 / 3 against 74
+// TFLOP/s).  The matrix instructions cut their sums, so the small products have sums of
+// their own and the weighted values of a tile are summed apart and added to the row's
+// in fp32.
+//
+// Fragments come 16 bytes at a time: the sums over d and over keys may take them in any
+// order, and a lane's four neighbouring values serve two instructions of Q K^T (d) or
+// four column tiles of P V (the columns of a tile are 4 apart).  The scores' own layout
+// then is P's operand layout.  One buffer each for K and V: a value tile loads during
+// Q K^T, the next key tile during P V.
+constexpr int kRows = 64, kKeys = 64, kF32Threads = 256;
 
 template <int D>
-struct Simt {
-    static constexpr int LD = D + 4;      // padded row of a Q or K tile (floats)
-    static constexpr int LP = kKeys + 4;  // padded row of the P tile (in the K tile's place)
-    static constexpr int kFloats = kRows * LD + kKeys * LD + kKeys * D;
-    static_assert(LP <= LD, "P in the place of K");
-    static constexpr int kBytes = kFloats * 4;
+struct F32 {
+    static constexpr int kCtas = 2;                         // per SM
+    static constexpr int CPR = D / 4;                       // 16-byte chunks per row
+    static constexpr int kBytes = ((kRows + 2 * kKeys) * D + kRows * kKeys) * 4;
 };
 
-template <typename T>
-__device__ __forceinline__ void load4(const T *src, float (&x)[4]) {
-    if constexpr (sizeof(T) == 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(src);
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-    } else {
-        const uint2 v = *reinterpret_cast<const uint2 *>(src);
-        x[0] = __uint_as_float(v.x << 16);
-        x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-        x[2] = __uint_as_float(v.y << 16);
-        x[3] = __uint_as_float(v.y & 0xFFFF0000u);
-    }
+// x in two tf32 parts, both cut (the matrix instruction reads a value's first 19 bits).
+// A NaN or infinite x has a NaN part: its products are NaN.
+__device__ __forceinline__ void tf32_parts(float x, uint32_t &hi, uint32_t &lo) {
+    hi = __float_as_uint(x) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kSimtThreads, 2)
-    varlen_simt_kernel(const __grid_constant__ VarlenParams p) {
-    using C = Simt<D>;
-    extern __shared__ float sm[];
-    float *sq = sm, *sk = sq + kRows * C::LD, *sv = sk + kKeys * C::LD, *sp = sk;
+// Float offset of chunk c of row r: rows of Q and K are read two at a time, four
+// chunks each, rows of V in pairs, four pairs by two chunks, without bank conflicts.
+template <int D>
+__device__ __forceinline__ int at_qk(int r, int c) {
+    return r * D + ((c ^ ((r & 1) << 2)) << 2);
+}
+template <int D>
+__device__ __forceinline__ int at_v(int r, int c) {
+    return r * D + ((c ^ (((r >> 1) & 3) << 1)) << 2);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kF32Threads, F32<D>::kCtas)
+    varlen_f32_kernel(const __grid_constant__ VarlenParams p) {
+    constexpr int CPR = F32<D>::CPR;
+    extern __shared__ __align__(16) float sm[];
+    __shared__ float row_part[2][kRows];            // of each half: maxima, at the end sums
+    float *sq = sm, *sk = sq + kRows * D, *sv = sk + kKeys * D;
     const int h = blockIdx.x % p.Hq, uu = blockIdx.x / p.Hq;
     const VarlenUnit U = load_unit(p, uu >> 1);
     const int r0 = (uu & 1) * kRows, rows = min(kRows, U.rows - r0);
-    if (rows <= 0) return;
-    const int g = h / p.G, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    if (rows <= 0) {
+        wait_previous_kernel();      // what follows in the stream may write k
+        return;
+    }
+    const int g = h / p.G, lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+    const int half = threadIdx.x >> 7, t = lane & 3, rl = lane >> 2;
     const int pos0 = U.pos0 + r0;
 
     // Q tile, rotated in fp32 (rows past the unit: zero)
-    const T *q = reinterpret_cast<const T *>(p.q) + (long long)(U.q0 + r0) * p.qs[0] + h * p.qs[1];
-    for (int i = threadIdx.x; i < kRows * (D / 2); i += kSimtThreads) {
+    const float *q = reinterpret_cast<const float *>(p.q) + (long long)(U.q0 + r0) * p.qs[0] +
+                     h * p.qs[1];
+    for (int i = threadIdx.x; i < kRows * (D / 2); i += kF32Threads) {
         const int r = i / (D / 2), pr = i % (D / 2);
         const int a = p.half ? pr : 2 * pr, b = p.half ? pr + D / 2 : 2 * pr + 1;
         float x = 0.f, y = 0.f, c = 1.f, s = 0.f;
         if (r < rows) {
-            x = static_cast<float>(q[(long long)r * p.qs[0] + a]);
-            y = static_cast<float>(q[(long long)r * p.qs[0] + b]);
+            x = q[(long long)r * p.qs[0] + a];
+            y = q[(long long)r * p.qs[0] + b];
             if (p.rotate_q) rope_sincos(pos0 + r, p.theta[pr], &c, &s);
         }
-        sq[r * C::LD + a] = x * c - y * s;
-        sq[r * C::LD + b] = x * s + y * c;
+        sq[at_qk<D>(r, a >> 2) + (a & 3)] = x * c - y * s;
+        sq[at_qk<D>(r, b >> 2) + (b & 3)] = x * s + y * c;
     }
-    float m[4], l[4];
-    float2 acc[4][D / 32];              // columns 64 c + 4 tx + {0, 1}, {2, 3}
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) acc[i][c] = make_float2(0.f, 0.f);
-    }
+    wait_previous_kernel();          // the rotated keys
+
     // keys any row of the tile sees: [0, jhi), without (sinks .. jlo) under a window
     const int last = pos0 + rows - 1;
     const int jhi = p.causal ? min(U.nk, last + 1) : U.nk;
     const int jlo = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
-    for (int j0 = 0; j0 < jhi; j0 += kKeys) {
-        if (j0 + kKeys <= jlo && j0 >= p.sinks) continue;
-        __syncthreads();
-        bool bad = false;               // some value of the tile is not finite
-        for (int i = threadIdx.x; i < kKeys * (D / 4); i += kSimtThreads) {
-            const int r = i / (D / 4), c = i % (D / 4) * 4;
-            float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
-            if (j0 + r < U.nk) {
-                const long long row = U.k0 + j0 + r;
-                load4(reinterpret_cast<const T *>(p.k) + row * p.ks[0] + g * p.ks[1] + c, x);
-                load4(reinterpret_cast<const T *>(p.v) + row * p.vs[0] + g * p.vs[1] + c, y);
-                // 0 x: zero, or NaN for an infinite or NaN value
-                const float z = 0.f * y[0] + 0.f * y[1] + 0.f * y[2] + 0.f * y[3];
-                bad |= z != 0.f;
-            }
-            *reinterpret_cast<float4 *>(sk + r * C::LD + c) = make_float4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<float4 *>(sv + r * D + c) = make_float4(y[0], y[1], y[2], y[3]);
+    auto seen_from = [&](int j) {    // the first tile from j on that is not hidden
+        return j + kKeys <= jlo && j >= p.sinks ? jlo / kKeys * kKeys : j;
+    };
+    const float *kb = reinterpret_cast<const float *>(p.k) + U.k0 * p.ks[0] + g * p.ks[1];
+    const float *vb = reinterpret_cast<const float *>(p.v) + U.k0 * p.vs[0] + g * p.vs[1];
+    // (a thread copies chunk threadIdx % CPR of every kStep-th row; rows behind the
+    // sequence read zero)
+    constexpr int kStep = kF32Threads / CPR;
+    const int cc = threadIdx.x % CPR, cr = threadIdx.x / CPR;
+    auto copy = [&](float *dst, const float *src, long long stride, int j0, bool value) {
+#pragma unroll
+        for (int i = 0; i < kKeys; i += kStep) {
+            const int r = cr + i, row = min(j0 + r, U.nk - 1);
+            cp_async16(smem_u32(dst + (value ? at_v<D>(r, cc) : at_qk<D>(r, cc))),
+                       src + row * stride + cc * 4, j0 + r < U.nk ? 16 : 0);
         }
-        bad = __syncthreads_or(bad);
-        // even and odd columns summed apart, two products an instruction
-        float2 s2[4][4];
+    };
+
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // rows rl, rl + 8 of the warp
+    float acc[D / 16][4];  // tile 4 G + e: columns half D/2 + 32 G + 4 (2 t + {0, 1}) + e
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s2[i][j] = make_float2(0.f, 0.f);
-#pragma unroll 4
-        for (int d = 0; d < D; d += 4) {
-            float4 a[4], b[4];
+        for (int c = 0; c < 4; ++c) acc[i][c] = 0.f;
+    const int wrow = warp * 16 + rl, pos = pos0 + wrow;
+    const float *qa = sq + wrow * D;
+    // the lane's weights, in P's operand layout: eight keys a chunk
+    float4 *sp = reinterpret_cast<float4 *>(sv + kKeys * D) + warp * (kKeys / 8) * 32 + lane;
+    constexpr int kN = kKeys / 16;   // score tiles of a warp
+
+    int j0 = seen_from(0);
+    if (j0 < jhi) copy(sk, kb, p.ks[0], j0, false);
+    cp_async_commit();
+    while (j0 < jhi) {
+        cp_async_wait<0>();
+        __syncthreads();             // the keys are there; the last values are read
+        copy(sv, vb, p.vs[0], j0, true);
+        cp_async_commit();
+        float s[kN][4], low[kN][4];  // (rl, rl + 8) x keys 32 half + 8 n + 2 t + {0, 1}
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                a[i] = *reinterpret_cast<const float4 *>(sq + (4 * ty + i) * C::LD + d);
+        for (int n = 0; n < kN; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                b[j] = *reinterpret_cast<const float4 *>(sk + (tx + 16 * j) * C::LD + d);
+            for (int c = 0; c < 4; ++c) s[n][c] = low[n][c] = 0.f;
+        // (not unrolled, here and over the keys below: the code of a key tile then stays
+        // in the instruction cache)
+#pragma unroll 1
+        for (int i = 0; i < D / 16; ++i) {
+            const int o = ((4 * i + t) ^ ((rl & 1) << 2)) << 2;
+            const float4 x = *reinterpret_cast<const float4 *>(qa + o);
+            const float4 y = *reinterpret_cast<const float4 *>(qa + 8 * D + o);
+            uint32_t u[kN][4], w[kN][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int n = 0; n < kN; ++n) {
+                const float4 k = *reinterpret_cast<const float4 *>(
+                    sk + (half * (kKeys / 2) + 8 * n + rl) * D + o);
+                tf32_parts(k.x, u[n][0], w[n][0]);
+                tf32_parts(k.y, u[n][1], w[n][1]);
+                tf32_parts(k.z, u[n][2], w[n][2]);
+                tf32_parts(k.w, u[n][3], w[n][3]);
+            }
+            uint32_t a0[4], b0[4], a1[4], b1[4];
+            tf32_parts(x.x, a0[0], b0[0]);
+            tf32_parts(y.x, a0[1], b0[1]);
+            tf32_parts(x.y, a0[2], b0[2]);
+            tf32_parts(y.y, a0[3], b0[3]);
+            tf32_parts(x.z, a1[0], b1[0]);
+            tf32_parts(y.z, a1[1], b1[1]);
+            tf32_parts(x.w, a1[2], b1[2]);
+            tf32_parts(y.w, a1[3], b1[3]);
+            // (products of one sum stand four and more instructions apart)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    s2[i][j] = fma2(make_float2(a[i].x, a[i].y), make_float2(b[j].x, b[j].y),
-                                    s2[i][j]);
-                    s2[i][j] = fma2(make_float2(a[i].z, a[i].w), make_float2(b[j].z, b[j].w),
-                                    s2[i][j]);
+            for (int n = 0; n < kN; ++n) mma_tf32(low[n], a0, w[n][0], w[n][1]);
+#pragma unroll
+            for (int n = 0; n < kN; ++n) mma_tf32(s[n], a0, u[n][0], u[n][1]);
+#pragma unroll
+            for (int n = 0; n < kN; ++n) mma_tf32(low[n], b0, u[n][0], u[n][1]);
+#pragma unroll
+            for (int n = 0; n < kN; ++n) mma_tf32(s[n], a1, u[n][2], u[n][3]);
+#pragma unroll
+            for (int n = 0; n < kN; ++n) mma_tf32(low[n], a1, w[n][2], w[n][3]);
+#pragma unroll
+            for (int n = 0; n < kN; ++n) mma_tf32(low[n], b1, u[n][2], u[n][3]);
+        }
+        auto sees = [&](int key, int at) {
+            return key < U.nk && (!p.causal || key <= at) &&
+                   (p.window <= 0 || at - key < p.window || key < p.sinks);
+        };
+        const int end = j0 + kKeys - 1, key0 = j0 + half * (kKeys / 2) + 2 * t;
+        const bool whole = end < U.nk && (!p.causal || end <= pos0) &&
+                           (p.window <= 0 || last - j0 < p.window || end < p.sinks);
+        float mx[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            mx[r] = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float &x = s[n][2 * r + e];
+                    x = whole || sees(key0 + 8 * n + e, pos + 8 * r)
+                            ? (x + low[n][2 * r + e]) * p.c_log2
+                            : -INFINITY;
+                    mx[r] = fmaxf(mx[r], x);
                 }
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+            if (t == 0) row_part[half][wrow + 8 * r] = mx[r];
         }
-        float s[4][4];
+        const int j1 = seen_from(j0 + kKeys);
+        __syncthreads();             // both halves' maxima are there, the keys are read
+        if (j1 < jhi) copy(sk, kb, p.ks[0], j1, false);
+        cp_async_commit();
+        float al[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] = s2[i][j].x + s2[i][j].y;
-        __syncthreads();                // every score is computed: P may replace the keys
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int pos = pos0 + 4 * ty + i;
-            float mx = -INFINITY;
-            bool seen[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int key = j0 + tx + 16 * j;
-                seen[j] = key < U.nk && (!p.causal || key <= pos) &&
-                          (p.window <= 0 || pos - key < p.window || key < p.sinks);
-                s[i][j] = seen[j] ? s[i][j] * p.c_log2 : -INFINITY;
-                mx = fmaxf(mx, s[i][j]);
-            }
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o, 16));
-            const float mn = fmaxf(m[i], mx);
-            const float al = m[i] == -INFINITY ? 0.f : exp2f(m[i] - mn);
+        for (int r = 0; r < 2; ++r) {
+            const float mn = fmaxf(m[r], fmaxf(mx[r], row_part[half ^ 1][wrow + 8 * r]));
+            al[r] = m[r] == -INFINITY ? 0.f : exp2f(m[r] - mn);
+            const float ref = mn == -INFINITY ? 0.f : mn;
             float z = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float w = s[i][j] == -INFINITY ? 0.f : exp2f(s[i][j] - mn);
-                z += w;
-                // (with non-finite values about, hidden weights are marked so that the
-                // product skips them)
-                sp[(4 * ty + i) * C::LP + tx + 16 * j] = seen[j] || !bad ? w : -1.f;
-            }
+            for (int n = 0; n < kN; ++n)
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o, 16);
-            m[i] = mn;
-            l[i] = l[i] * al + z;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) acc[i][c] = mul2(acc[i][c], make_float2(al, al));
-        }
-        __syncthreads();
-#pragma unroll 2
-        for (int j = 0; j < kKeys; j += 4) {
-            float w[4][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 y = *reinterpret_cast<const float4 *>(sp + (4 * ty + i) * C::LP + j);
-                w[i][0] = y.x; w[i][1] = y.y; w[i][2] = y.z; w[i][3] = y.w;
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    const float4 v =
-                        *reinterpret_cast<const float4 *>(sv + (j + k) * D + 64 * c + 4 * tx);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (bad && w[i][k] == -1.f) continue;
-                        const float2 w2 = make_float2(w[i][k], w[i][k]);
-                        acc[i][2 * c] = fma2(w2, make_float2(v.x, v.y), acc[i][2 * c]);
-                        acc[i][2 * c + 1] = fma2(w2, make_float2(v.z, v.w), acc[i][2 * c + 1]);
-                    }
+                for (int e = 0; e < 2; ++e) {
+                    float &x = s[n][2 * r + e];
+                    x = exp2f(x - ref);
+                    z += x;
                 }
+            m[r] = mn;
+            l[r] = l[r] * al[r] + z;
         }
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+            sp[(half * kN + n) * 32] = make_float4(s[n][0], s[n][2], s[n][1], s[n][3]);
+        cp_async_wait<1>();
+        // An infinite or NaN value would reach rows that do not see it, by 0 x: a tile
+        // that holds one is cleared of it, and the rows that see it add it.
+        float z = 0.f;
+#pragma unroll
+        for (int i = 0; i < kKeys; i += kStep) {
+            const float4 x = *reinterpret_cast<const float4 *>(sv + at_v<D>(cr + i, cc));
+            z += 0.f * x.x + 0.f * x.y + 0.f * x.z + 0.f * x.w;
+        }
+        const bool bad = __syncthreads_or(z != 0.f);   // values and weights are there
+        if (bad) {
+#pragma unroll 1
+            for (int i = 0; i < kKeys; i += kStep) {
+                float4 &x = *reinterpret_cast<float4 *>(sv + at_v<D>(cr + i, cc));
+                x.x = fabsf(x.x) < INFINITY ? x.x : 0.f;
+                x.y = fabsf(x.y) < INFINITY ? x.y : 0.f;
+                x.z = fabsf(x.z) < INFINITY ? x.z : 0.f;
+                x.w = fabsf(x.w) < INFINITY ? x.w : 0.f;
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int G = 0; G < D / 64; ++G) {
+            float o[4][4], low[4][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[e][c] = low[e][c] = 0.f;
+            const float *vr = sv + 2 * t * D + (((half * CPR / 2 + 8 * G + rl) ^ (2 * t)) << 2);
+#pragma unroll 2
+            for (int n = 0; n < kKeys / 8; ++n) {
+                const float4 w = sp[n * 32];
+                const float4 x = *reinterpret_cast<const float4 *>(vr + 8 * n * D);
+                const float4 y = *reinterpret_cast<const float4 *>(vr + 8 * n * D + D);
+                uint32_t a[4], b[4];
+                tf32_parts(w.x, a[0], b[0]);
+                tf32_parts(w.y, a[1], b[1]);
+                tf32_parts(w.z, a[2], b[2]);
+                tf32_parts(w.w, a[3], b[3]);
+                const float v0[4] = {x.x, x.y, x.z, x.w}, v1[4] = {y.x, y.y, y.z, y.w};
+                uint32_t u0[4], w0[4], u1[4], w1[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    tf32_parts(v0[e], u0[e], w0[e]);
+                    tf32_parts(v1[e], u1[e], w1[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mma_tf32(low[e], a, w0[e], w1[e]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mma_tf32(o[e], a, u0[e], u1[e]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mma_tf32(low[e], b, u0[e], u1[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    acc[4 * G + e][c] =
+                        fmaf(acc[4 * G + e][c], al[c >> 1], o[e][c] + low[e][c]);
+        }
+        if (bad) {
+#pragma unroll 1
+            for (int r = 0; r < min(kKeys, U.nk - j0); ++r)
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float x = vb[(j0 + r) * p.vs[0] + half * (D / 2) + 32 * (i / 4) +
+                                           4 * (2 * t + c) + i % 4];
+                        if (fabsf(x) < INFINITY) continue;
+                        if (sees(j0 + r, pos)) acc[i][c] += x;
+                        if (sees(j0 + r, pos + 8)) acc[i][2 + c] += x;
+                    }
+        }
+        j0 = j1;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 4 * ty + i;
-        if (r >= rows) continue;
+    for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        if (t == 0) row_part[half][wrow + 8 * r] = l[r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int i = wrow + 8 * r;
+        if (i >= rows) continue;
+        const float z = row_part[0][i] + row_part[1][i];
         // a NaN sum (a NaN or infinite score the row does see) stays NaN
-        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
-        const long long row = U.q0 + r0 + r;
-        T *dst = reinterpret_cast<T *>(p.o) + row * p.os[0] + h * p.os[1];
+        const float inv = z == 0.f ? 0.f : 1.f / z;
+        const long long row = U.q0 + r0 + i;
+        float *dst = reinterpret_cast<float *>(p.o) + row * p.os[0] + h * p.os[1] +
+                     half * (D / 2) + 8 * t;
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-            const float2 x = acc[i][2 * c], y = acc[i][2 * c + 1];
-            const float o[4] = {x.x * inv, x.y * inv, y.x * inv, y.y * inv};
+        for (int G = 0; G < D / 64; ++G)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dst[64 * c + 4 * tx + e] = static_cast<T>(o[e]);
-        }
-        if (p.lse && tx == 0)
+            for (int c = 0; c < 2; ++c)
+                *reinterpret_cast<float4 *>(dst + 32 * G + 4 * c) = make_float4(
+                    acc[4 * G][2 * r + c] * inv, acc[4 * G + 1][2 * r + c] * inv,
+                    acc[4 * G + 2][2 * r + c] * inv, acc[4 * G + 3][2 * r + c] * inv);
+        if (p.lse && t == 0 && half == 0)
             p.lse[(long long)h * p.Tq + row] =
-                l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718055994531f;
+                z == 0.f ? -INFINITY : (m[r] + log2f(z)) * 0.69314718055994531f;
     }
 }
 
-template <typename T, int D>
-lcx_status launch_simt(const VarlenParams &p, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(varlen_simt_kernel<T, D>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Simt<D>::kBytes);
+template <int D>
+lcx_status launch_f32(const VarlenParams &p, bool after_keys, cudaStream_t s) {
+    auto kern = varlen_f32_kernel<D>;
+    cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F32<D>::kBytes);
     if (e != cudaSuccess)
         return fail(LCX_ERR_CUDA, "cudaFuncSetAttribute failed: %s", cudaGetErrorString(e));
     const long long grid = 2ll * p.n_units * p.Hq;
     if (grid > 0x7fffffffLL) return fail(LCX_ERR_UNSUPPORTED, "too many work units");
-    varlen_simt_kernel<T, D><<<unsigned(grid), kSimtThreads, Simt<D>::kBytes, s>>>(p);
-    e = cudaGetLastError();
+    if (after_keys)
+        e = launch_dependent(kern, dim3(unsigned(grid)), dim3(kF32Threads), F32<D>::kBytes, s, p);
+    else
+        kern<<<unsigned(grid), kF32Threads, F32<D>::kBytes, s>>>(p);
+    if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess)
         return fail(LCX_ERR_CUDA, "attn_varlen launch failed: %s", cudaGetErrorString(e));
     return LCX_OK;
@@ -1588,7 +1711,8 @@ extern "C" lcx_status lcx_attn_varlen(const lcx_varlen_args *a, void *stream) {
     p.units = reinterpret_cast<const VarlenUnit *>(
         a->plan + plan_units(a->info.n_seqs, 0, a->info.n_units[0]));
     p.n_units = int(a->info.n_units[0]);
-    return a->D == 128 ? launch_simt<float, 128>(p, s) : launch_simt<float, 64>(p, s);
+    const bool dep = p.rotate_q && a->info.total_k > 0;
+    return a->D == 128 ? launch_f32<128>(p, dep, s) : launch_f32<64>(p, dep, s);
 }
 
 extern "C" int64_t lcx_varlen_workspace_bytes(const lcx_varlen_info *info, int64_t Hkv, int64_t D,

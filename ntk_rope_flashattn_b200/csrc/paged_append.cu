@@ -17,6 +17,7 @@
 
 #include "paged.cuh"
 #include "rope_angle.cuh"
+#include "sm100.cuh"
 #include "vec16.cuh"
 
 namespace lcx {
@@ -123,6 +124,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     constexpr int N = Vec<T>::N;
     constexpr int NP = kHalf ? N : N / 2;           // pairs per job
     __shared__ Place place[kThreads];
+    pdl_launch_dependents();       // attention over packed fp32 rows may be scheduled
     const int t0 = blockIdx.x * a.rows;
     const int job = threadIdx.x % a.jobs, row = threadIdx.x / a.jobs, t = t0 + row;
     const bool in = row < a.rows && t < a.T;

@@ -32,7 +32,8 @@ def plain(q, k, v, lq, lk, rope, causal=True, window=0, sinks=0, scale=None, pre
 def arithmetic(dtype, n):
     """(u_s, u_p): bf16 inputs: q' and k' rounded to fp16 (2^-11 each), their products'
     sums cut by the tensor core, the weights rounded to bf16 (their sum is not); fp32
-    rounds nothing but its sums (and q', k' to fp32)."""
+    cuts each factor into two tf32 parts (2^-21 each, 2^-20 for the product left out:
+    2^-19, within acc for the logits and 2 u_p for the values) and rounds q', k' to fp32."""
     acc = 128 * 2.0 ** -23 + 2.0 ** -18
     if dtype == torch.bfloat16:
         return 2.0 ** -10 + 2.0 ** -20 + acc, 2.0 ** -8 + n * 2.0 ** -23 + 2.0 ** -20
