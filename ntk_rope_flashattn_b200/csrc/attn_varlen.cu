@@ -1373,7 +1373,9 @@ lcx_status token_map(CUtensorMap *map, const void *ptr, int64_t T, int64_t H, in
     EncodeTiledFn fn = encode_fn();
     if (!fn) return fail(LCX_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
     const cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(T), cuuint64_t(H), 1};
-    const cuuint64_t strides[3] = {cuuint64_t(st[0] * 2), cuuint64_t(st[1] * 2), 16};
+    // (a single token's or head's stride is never taken)
+    const cuuint64_t strides[3] = {cuuint64_t(T > 1 ? st[0] * 2 : D * 2),
+                                   cuuint64_t(H > 1 ? st[1] * 2 : D * 2), 16};
     const cuuint32_t box[4] = {64, 128, 1, 1}, ones[4] = {1, 1, 1, 1};
     const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims,
                           strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1579,9 +1581,16 @@ lcx_status varlen_prepare(const lcx_varlen_args *a, VarlenParams &p, bool *noop)
         return fail(LCX_ERR_INVALID_ARG, "plan must be a 16-byte aligned device pointer");
     if ((st = check_tokens(a->q, a->q_strides, es, "q")) != LCX_OK) return st;
     if ((st = check_tokens(a->o, a->o_strides, es, "o")) != LCX_OK) return st;
+    if ((st = check_distinct(a->o_strides, a->Tq, a->Hq, "o")) != LCX_OK) return st;
     if (I.total_k > 0) {
         if ((st = check_tokens(a->k, a->k_strides, es, "k")) != LCX_OK) return st;
         if ((st = check_tokens(a->v, a->v_strides, es, "v")) != LCX_OK) return st;
+    }
+    if (es == 2) {               // a tensor map's strides are positive
+        if ((st = check_distinct(a->q_strides, a->Tq, a->Hq, "q")) != LCX_OK ||
+            (st = check_distinct(a->k_strides, a->Tk, a->Hkv, "k")) != LCX_OK ||
+            (st = check_distinct(a->v_strides, a->Tk, a->Hkv, "v")) != LCX_OK)
+            return st;
     }
     const bool rotate = !(a->flags & LCX_VARLEN_PREROTATED) && a->rope.mode != LCX_ROPE_NONE;
     if (rotate && I.total_k > 0) {
@@ -1653,7 +1662,6 @@ extern "C" lcx_status lcx_varlen_plan(const int32_t *lens_q, const int32_t *lens
         return fail(LCX_ERR_INVALID_ARG, "plan holds %lld int32; %lld needed", (long long)ints,
                     (long long)x.ints);
     memset(plan, 0, size_t(x.ints) * 4);
-    plan[0] = kPlanMagic;
     int32_t *cu_q = plan + plan_cu_q(), *cu_k = plan + plan_cu_k(n);
     for (int64_t s = 0; s < n; ++s) {
         cu_q[s + 1] = cu_q[s] + lens_q[s];

@@ -47,6 +47,8 @@ lcx_status paged_prepare(const lcx_paged_cache *c, PagedParams &x);
 
 // Shared argument checks: a tensor of (token, head, dim) strides in elements.
 lcx_status check_tokens(const void *ptr, const int64_t *st, int es, const char *name);
+// Refuses a tensor whose tokens or heads share memory (stride 0).
+lcx_status check_distinct(const int64_t *st, int64_t tokens, int64_t heads, const char *name);
 
 // Launch `kern` as a programmatic dependent of the stream's previous kernel: it
 // may be scheduled while that one ends and waits (griddepcontrol.wait) for its

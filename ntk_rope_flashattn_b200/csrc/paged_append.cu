@@ -283,8 +283,10 @@ extern "C" lcx_status lcx_paged_append(const lcx_paged_cache *cache,
         if (g->Hq == 0) return fail(LCX_ERR_INVALID_ARG, "q without heads");
         if ((st = check_tokens(g->q, g->q_strides, p.es, "q")) != LCX_OK) return st;
         if ((st = check_tokens(g->q_out, g->q_out_strides, p.es, "q_out")) != LCX_OK) return st;
+        if ((st = check_distinct(g->q_out_strides, g->T, g->Hq, "q_out")) != LCX_OK) return st;
     }
-    if (g->k_out && (st = check_tokens(g->k_out, g->k_out_strides, p.es, "k_out")) != LCX_OK)
+    if (g->k_out && ((st = check_tokens(g->k_out, g->k_out_strides, p.es, "k_out")) != LCX_OK ||
+                     (st = check_distinct(g->k_out_strides, g->T, p.H, "k_out")) != LCX_OK))
         return st;
     for (int d = 0; d < 2; ++d)
         if ((g->q && g->q == g->q_out && g->q_strides[d] != g->q_out_strides[d]) ||

@@ -978,6 +978,7 @@ extern "C" lcx_status lcx_paged_decode(const lcx_paged_cache *cache,
     if (!g->seq_ids) return fail(LCX_ERR_INVALID_ARG, "seq_ids is NULL");
     if ((st = check_tokens(g->q, g->q_strides, c.es, "q")) != LCX_OK) return st;
     if ((st = check_tokens(g->o, g->o_strides, c.es, "o")) != LCX_OK) return st;
+    if ((st = check_distinct(g->o_strides, g->n, g->Hq, "o")) != LCX_OK) return st;
     if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
         return fail(LCX_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
     if (workspace_bytes < need)

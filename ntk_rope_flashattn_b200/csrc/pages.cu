@@ -484,6 +484,12 @@ lcx_status check_tokens(const void *ptr, const int64_t *st, int es, const char *
     return LCX_OK;
 }
 
+lcx_status check_distinct(const int64_t *st, int64_t tokens, int64_t heads, const char *name) {
+    if ((st[0] == 0 && tokens > 1) || (st[1] == 0 && heads > 1))
+        return fail(LCX_ERR_UNSUPPORTED, "%s: stride 0", name);
+    return LCX_OK;
+}
+
 lcx_status paged_prepare(const lcx_paged_cache *c, PagedParams &x) {
     if (!c) return fail(LCX_ERR_INVALID_ARG, "cache is NULL");
     if (c->dtype != LCX_BF16 && c->dtype != LCX_F32)

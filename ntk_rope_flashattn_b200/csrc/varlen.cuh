@@ -8,7 +8,7 @@
 
 namespace lcx {
 
-// Plan layout (int32): header of 8, cu_q[n + 1], cu_k[n + 1], then, from a
+// Plan layout (int32): 8 zeros, cu_q[n + 1], cu_k[n + 1], then, from a
 // 16-byte boundary each, the units of 128 and of 256 query rows, heaviest first.
 struct VarlenUnit {
     int q0, rows;     // first packed query row, rows (1..128 or 1..256)
@@ -17,8 +17,6 @@ struct VarlenUnit {
     int pad[3];
 };
 static_assert(sizeof(VarlenUnit) == 32, "plan layout");
-
-constexpr int kPlanMagic = 0x766c6370;
 
 inline int64_t plan_cu_q() { return 8; }
 inline int64_t plan_cu_k(int64_t n) { return 8 + n + 1; }

@@ -17,6 +17,7 @@ page) skips the entry and is reported through the optional ``status`` tensor
 (one int32; written, never cleared).
 """
 import ctypes
+import functools
 
 from . import RopeParams, _check, _dtype_code, _RopeParams, _same_device, load
 
@@ -68,6 +69,12 @@ def _declare(lib):
     lib.lcx_paged_append.restype = lib.lcx_paged_decode.restype = ctypes.c_int
 
 
+_FIXED = frozenset(("k_pages", "v_pages", "meta", "block_table", "seq_lens", "ref_counts",
+                    "free_pages", "n_free", "scratch", "num_pages", "page_size", "kv_heads",
+                    "head_dim", "max_seqs", "max_pages_per_seq", "num_layers", "dtype", "device",
+                    "_struct"))
+
+
 class PagedCache:
     """A key/value cache in pages (mirrors ``lcx_paged_cache``).
 
@@ -116,9 +123,16 @@ class PagedCache:
         self.free_pages = self.meta[a + b + p:a + b + 2 * p]
         self.n_free = self.meta[a + b + 2 * p:]
         self.scratch = torch.zeros(n_scratch, dtype=torch.int32, device=device)
-        self._struct = ctypes.byref(self._c())     # the buffers never change
+        self._struct = ctypes.byref(self._c())
         self._workspace_bytes = {}
         self.reset()
+
+    def __setattr__(self, name, value):
+        # the C struct holds the buffers' addresses
+        if ("_struct" in self.__dict__ and name in _FIXED and
+                value is not self.__dict__[name]):
+            raise AttributeError("%s of a PagedCache does not change (copy into it)" % name)
+        object.__setattr__(self, name, value)
 
     def reset(self):
         """Empty the cache: every page free, every sequence without tokens."""
@@ -238,18 +252,19 @@ def _strides3(t):
     return _Strides3(*t.stride())
 
 
+@functools.lru_cache(maxsize=64)
+def _rope_struct(*fields):
+    return RopeParams(*fields)._c()
+
+
 def _rope_c(rope):
-    """The rope's C struct, kept on it while its fields stay the same (factor
-    tables may change in place: built anew)."""
+    """The rope's C struct, one per set of field values (factor tables may change in
+    place: built anew)."""
     if rope.factors is not None or rope.factors_short is not None:
         return rope._c()
-    key = (rope.mode, rope.head_dim, rope.base, rope.scale, rope.original_max_pos, rope.alpha,
-           rope.beta, rope.pairing, rope.seq_len)
-    kept = rope.__dict__.get("_kept")
-    if kept is None or kept[0] != key:
-        kept = (key, rope._c())
-        rope.__dict__["_kept"] = kept
-    return kept[1]
+    return _rope_struct(rope.mode, int(rope.head_dim), float(rope.base), float(rope.scale),
+                        int(rope.original_max_pos), float(rope.alpha), float(rope.beta),
+                        rope.pairing, int(rope.seq_len))
 
 
 def paged_append(cache, k, v, seq_ids, start, rope: RopeParams, layer: int = 0, cu_new=None,

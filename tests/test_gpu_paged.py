@@ -465,3 +465,14 @@ def test_decode_step_replays_from_a_graph():
         want = step(b, None)
         assert torch.equal(o, want)
         assert torch.equal(a.seq_lens, b.seq_lens)
+
+
+def test_a_cache_keeps_its_buffers():
+    """The calls hold the buffers' addresses: a cache refuses other ones."""
+    cache = lcx.PagedCache(4, 16, 2, 64, 2, 2)
+    for name in ("k_pages", "block_table", "page_size"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, getattr(lcx.PagedCache(4, 16, 2, 64, 2, 2), name)
+                    if name != "page_size" else 32)
+    cache.seq_lens += 0          # in place
+    cache.reset()

@@ -211,6 +211,50 @@ def test_many_sequences_hidden_values_and_scaled_keys(Hq, H, D):
     compare(o, lse, plain(qs, ks, v, MANY, MANY, rope), torch.bfloat16, 511)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_one_token_and_one_head_of_any_stride(dt):
+    """Strides of sizes of one are never taken."""
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    rope = lcx.RopeParams("plain", 64)
+    q, k, v = (randn(i, 1, h, 64, dtype=dtype) for i, h in ((1, 4), (2, 1), (3, 1)))
+    k, v = (t.as_strided(t.shape, (0, 0, 1)) for t in (k, v))
+    o, lse = lcx.attn_varlen(q, k, v, lcx.VarlenPlan([1]), rope, return_lse=True)
+    compare(o, lse, plain(q, k, v, [1], [1], rope), dtype, 1)
+
+
+def test_expanded_heads_fp32():
+    """One kv head expanded to all: read as it stands (fp32)."""
+    rope = lcx.RopeParams("plain", 64)
+    lens = [70, 30]
+    q, k, v = (randn(i, 100, h, 64, dtype=torch.float32) for i, h in ((1, 4), (2, 1), (3, 1)))
+    plan = lcx.VarlenPlan(lens)
+    a = lcx.attn_varlen(q, k, v, plan, rope)
+    b = lcx.attn_varlen(q, k.expand(-1, 4, -1), v.expand(-1, 4, -1), plan, rope)
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_fp32_values_not_finite(D):
+    """fp32: a NaN and an infinite value in two columns reach the queries that see
+    them in those columns, over several key tiles, and nothing else."""
+    rope = lcx.RopeParams("plain", D)
+    q, k, v = (randn(i, 300, h, D, dtype=torch.float32) for i, h in ((1, 4), (2, 2), (3, 2)))
+    plan = lcx.VarlenPlan([40, 260])
+    for window in (0, 100):
+        a = lcx.attn_varlen(q, k, v, plan, rope, window=window)
+        v2 = v.clone()
+        v2[140, 1, 7] = float("nan")         # token 100 of the second sequence
+        v2[140, 0, D - 1] = -float("inf")
+        b = lcx.attn_varlen(q, k, v2, plan, rope, window=window)
+        last = 300 if window == 0 else 140 + window
+        hit = torch.zeros_like(a, dtype=torch.bool)
+        hit[140:last, 2:, 7] = True
+        hit[140:last, :2, D - 1] = True
+        assert torch.isnan(b[140:last, 2:, 7]).all()
+        assert (b[140:last, :2, D - 1] == -float("inf")).all()
+        assert torch.equal(a[~hit], b[~hit])
+
+
 def test_nan_value_of_one_column():
     """A NaN in one column of one visible value reaches that column of the queries
     that see it, and nothing else."""

@@ -269,6 +269,38 @@ def test_varlen_without_rows_is_a_noop(lib):
     assert lib.lcx_attn_varlen(ctypes.byref(a), None) == lcx.LCX_OK
 
 
+@pytest.mark.parametrize("bad", [[0, 128, 1], [8 * 128, 0, 1]])
+def test_expanded_outputs_are_refused(lib, bad):
+    """Tokens or heads that share memory: outputs of every call, and what the bf16
+    packed call reads through tensor maps."""
+    c = ctypes.byref(cache_args())
+    for a in (append_args(q=F, q_out=F + (1 << 20), Hq=8, q_out_strides=bad),
+              append_args(k_out=F + (1 << 20), k_out_strides=bad)):
+        assert lib.lcx_paged_append(c, ctypes.byref(a), None) == UNS
+    a = decode_args(o_strides=bad)
+    assert lib.lcx_paged_decode(c, ctypes.byref(a), F, 1 << 40, None) == UNS
+    for name in ("o", "q", "k", "v"):
+        a = varlen_args(**{name + "_strides": bad})
+        assert lib.lcx_attn_varlen(ctypes.byref(a), None) == UNS
+    a = varlen_args(dtype=1, o_strides=bad)
+    assert lib.lcx_attn_varlen(ctypes.byref(a), None) == UNS
+    assert b"stride 0" in lib.lcx_last_error()
+
+
+def test_rope_struct_follows_the_fields():
+    """One struct per set of values; the parameters stay plain data."""
+    import copy
+    import pickle
+    r = rope(mode="yarn", scale=4.0)
+    a = paged._rope_c(r)
+    assert bytes(a) == bytes(r._c()) and paged._rope_c(r) is a
+    assert pickle.loads(pickle.dumps(r)) == r == copy.deepcopy(r)
+    r.scale = 8.0
+    assert bytes(paged._rope_c(r)) == bytes(r._c()) != bytes(a)
+    f = rope(mode="factors", factors=np.ones(64))
+    assert paged._rope_c(f) is not paged._rope_c(f)
+
+
 def test_binding_refuses_host_tensors():
     q = torch.zeros((4, 2, 64))
     plan = lcx.VarlenPlan([4], device="cpu")
