@@ -3,7 +3,9 @@
  * (liblcx.so, sm_100a).
  *
  * Three calls make up the hot path (lcx_attn_fwd_split and lcx_attn_merge
- * add split-KV evaluation for decode-sized problems):
+ * add split-KV evaluation for decode-sized problems; for serving, lcx_attn_varlen
+ * takes packed prompts of different lengths, and lcx_pages_*, lcx_paged_append and
+ * lcx_paged_decode keep and read a cache in pages):
  *   lcx_rope_table  per-pair RoPE frequencies theta'_i and the attention scale
  *                   for plain RoPE, Position Interpolation, NTK-aware base
  *                   scaling and YaRN (NTK-by-parts ramp + 0.1 ln s + 1).
@@ -489,11 +491,15 @@ typedef struct {
 
 /*
  * lcx_paged_append -- rotate the new tokens' keys (times mscale, as
- * lcx_apply_rope does) and write keys and values into their pages of one layer; optionally rotate the tokens' queries in the same pass.  Entry
- * i's k-th token sits at position start[i] + k; a position at or beyond the
- * sequence's length is not written (LCX_ERR_INVALID_ARG in the status word:
- * extend first).  Rows of skipped entries and rows outside cu_new are neither
- * read nor written.  Each position must be given once per call.
+ * lcx_apply_rope does) and write keys and values into their pages of one layer;
+ * optionally rotate the tokens' queries in the same pass.  Entry i's k-th token
+ * sits at position start[i] + k; a position at or beyond the sequence's length is
+ * not written (LCX_ERR_INVALID_ARG in the status word: extend first).  Rows of
+ * skipped entries and rows outside cu_new are not written (rows below T may be
+ * read).  Each position must be given once per call.
+ *   Angles (here, in lcx_paged_decode and in lcx_attn_varlen) come from fp64
+ *   frequencies, not from lcx_rope_table's fp32 values, whose rounding moves the
+ *   angle at position m by up to m 2^-25.
  */
 LCX_API lcx_status lcx_paged_append(const lcx_paged_cache *cache,
                                     const lcx_paged_append_args *args, void *stream);
@@ -531,9 +537,9 @@ LCX_API int64_t lcx_paged_decode_workspace_bytes(int64_t n, int64_t Hq, int64_t 
  * never read.  seq_ids may name one sequence several times.
  *   Supported: D 64 or 128, any Hq / Hkv; strides multiples of 16 bytes.
  *   Arithmetic: 16-bit pools: bf16 tensor-core products with fp32
- *   accumulation; with at most 8 query heads per kv head q' and the weights
- *   enter as two bf16 parts each (16 bits of mantissa), else rounded to bf16.
- *   fp32 pools: every operand as two tf32 parts (about 21 bits).
+ *   accumulation; q' enters as two bf16 parts (16 bits of mantissa), the weights
+ *   too with at most 8 query heads per kv head, else rounded to bf16 (their sum
+ *   is not).  fp32 pools: every operand as two tf32 parts (within 2^-21 of it).
  *   workspace : DEVICE, 256-byte aligned, lcx_paged_decode_workspace_bytes;
  *               contents ignored and overwritten; not shared by calls in flight.
  */
@@ -602,12 +608,13 @@ typedef struct {
  * keys) gets o = 0, lse = -inf.  Rows of o and lse at total_q and beyond are
  * left as they were.  NaN or infinity in a key or value that a query does not
  * see leaves that query alone.
- *   Supported: D 64 or 128, full rotary.
+ *   Supported: D 64 or 128, full rotary; o does not overlap k or v; bf16: no
+ *   stride of 0.
  *   Arithmetic: bf16: tensor-core products with fp32 accumulation; q' and k'
  *   rounded to fp16 (rows out of its range scaled by a power of two), in two fp16
  *   parts for row blocks that start before position 127 or see fewer keys; given
  *   rotated inputs enter as they are; the weights rounded to bf16, their sum not.
- *   fp32: fp32 products.
+ *   fp32: every operand of a product as two tf32 parts (within 2^-21 of it).
  *   dev_status: LCX_ERR_TIMEOUT after an expired wait, as lcx_attn_fwd (o and lse
  *   are then undefined); LCX_ERR_INVALID_ARG for a plan that is not info's.
  */

@@ -7,12 +7,20 @@
 //
 // bf16: the tcgen05 kernel described here; fp32: the kernel of tf32 products below.
 //
-// The tcgen05 kernel is bound by the tensor core (4 D flops per visible pair and
-// query head) and, per key tile, by the softmax's 128 x 128 exponentials per query
-// tile.  One CTA per (row block of the plan, pair of query heads), 16 warps:
-//   warps 0-3, 4-7  softmax of query tile 0, 1: one thread per row
-//   warps 8-11      helpers: rotate the query tiles; clean the value tiles at a border
+// The tcgen05 kernel has a floor of 4 D flops per visible pair and query head on the
+// tensor core and, as much again, 128 x 128 exponentials per query and key tile; a
+// tile of scores goes through both in turn.  Measured: 4.2k cycles per key tile (2048
+// of tensor-core work) and 14-16k per CTA outside of the key loop, the query's copy,
+// rotation and the output.  16384 tokens of 32 heads: 1030 TFLOP/s (2.1 ms); 12
+// prompts of 200 to 4100: 600 TFLOP/s (386 us); 8 x 2048: 671.  (Persistent CTAs whose
+// helpers rotate the next block's queries meanwhile: 560-612 us where this takes 410.
+// The rotation's warps take issue slots from the softmax: 4.7-5.8k cycles per tile.)
+// One CTA per (row block of the plan, pair of query heads), 16 warps:
+//   warps 0-3, 4-7  rotate the query tiles, then softmax of query tile 0, 1: one
+//                   thread per row
+//   warps 8-11      helpers: rotate along; clean the value tiles at a border
 //   warp 12 / 14    TMA producers of Q and K / of V;  warp 13  MMA issuer
+//   warp 15         looks whether keys are scaled
 // Both tiles multiply the same key tiles, so a K/V tile is loaded once for 256
 // query rows, and one tile's softmax overlaps the other's products (order PV0(j),
 // S0(j + 1), PV1(j), S1(j + 1)).  With an odd group the two tiles are consecutive
@@ -64,7 +72,10 @@ namespace {
 // order, and a lane's four neighbouring values serve two instructions of Q K^T (d) or
 // four column tiles of P V (the columns of a tile are 4 apart).  The scores' own layout
 // then is P's operand layout.  One buffer each for K and V: a value tile loads during
-// Q K^T, the next key tile during P V.
+// Q K^T, the next key tile during P V.  Two CTAs, 16 warps, per SM: bound by the issue
+// of the parts' arithmetic and its latency (four warps of twice the work each: 12 %
+// slower, at small sizes 40 %).  4 x 1024 tokens, 32 heads of 128: 745 us, 46 TFLOP/s
+// (fp32 products on the FMA pipe: 1075 us).
 constexpr int kRows = 64, kKeys = 64, kF32Threads = 256;
 
 template <int D>
@@ -1485,8 +1496,8 @@ lcx_status run_tc(const lcx_varlen_args *a, const VarlenParams &v, cudaStream_t 
         k.T = int(I.total_k);
         k.H = v.Hkv;
         k.all_lo = v.window > 0 && v.window < 128;
-        rope_freqs_unchecked(&a->rope, effective_seq_len(&a->rope, std::max<int64_t>(I.max_k, 1)),
-                             k.theta, &k.ms);
+        memcpy(k.theta, v.theta, sizeof(k.theta));
+        k.ms = v.ms;
         lcx_status st = a->D == 128 ? (half ? launch_keys<128, true>(k, s) : launch_keys<128, false>(k, s))
                                     : (half ? launch_keys<64, true>(k, s) : launch_keys<64, false>(k, s));
         if (st != LCX_OK) return st;
@@ -1627,13 +1638,15 @@ lcx_status varlen_prepare(const lcx_varlen_args *a, VarlenParams &p, bool *noop)
     p.sinks = p.window > 0 ? int(std::min(a->sinks, big)) : 0;
     p.rotate_q = rotate ? 1 : 0;
     p.half = a->rope.pairing == LCX_PAIR_HALF;
-    float ms = 1.f;
-    rope_freqs_unchecked(&a->rope, effective_seq_len(&a->rope, std::max<int64_t>(I.max_k, 1)),
-                         p.theta, &ms);
+    p.ms = 1.f;
+    if (rotate)
+        rope_freqs_unchecked(&a->rope,
+                             effective_seq_len(&a->rope, std::max<int64_t>(I.max_k, 1)), p.theta,
+                             &p.ms);
     const double scale =
         a->softmax_scale > 0.f ? double(a->softmax_scale) : 1.0 / std::sqrt(double(a->D));
     // q' is rotated without mscale (folded in here); the rotated keys carry theirs
-    p.c_log2 = float(scale * (rotate ? double(ms) : 1.0) * 1.4426950408889634);
+    p.c_log2 = float(scale * double(p.ms) * 1.4426950408889634);
     p.timeout_ns = 1000000ull * (unsigned long long)(a->watchdog_ms > 0 ? a->watchdog_ms : 2000);
     return LCX_OK;
 }

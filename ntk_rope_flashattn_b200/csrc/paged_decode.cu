@@ -7,7 +7,10 @@
 // (8.3.5 step 3).
 //
 // Bound by HBM: every visible key and value is read once, 4 Hkv D bytes per key
-// (bf16) against 4 Hq D flops.
+// (bf16) against 4 Hq D flops.  Measured (8 kv heads of 128, bf16): 1.39 GB of keys and
+// values in 208 us, 6.7 TB/s, as fast as a copy; 0.35 GB in 64.5 us, 5.4 TB/s (the start,
+// the uneven end and the join are 11 us); 4 short sequences in 7.6 us.  fp32: 0.40 GB
+// in 89 us, 4.5 TB/s.
 //
 // Work: the visible keys of each (entry, kv head, block of query heads), a
 // "segment", are cut into blocks of 32 to 128 keys; the blocks of all segments in
@@ -1018,10 +1021,10 @@ extern "C" lcx_status lcx_paged_decode(const lcx_paged_cache *cache,
     p.rotate = (g->flags & LCX_DECODE_PREROTATED) || g->rope.mode == LCX_ROPE_NONE ? 0 : 1;
     p.half = g->rope.pairing == LCX_PAIR_HALF;
     float ms = 1.f;
-    rope_freqs_unchecked(&g->rope, g->rope.seq_len, p.theta, &ms);
+    if (p.rotate) rope_freqs_unchecked(&g->rope, g->rope.seq_len, p.theta, &ms);
     const double scale =
         g->softmax_scale > 0.f ? double(g->softmax_scale) : 1.0 / std::sqrt(double(c.D));
-    p.c_log2 = float(scale * (p.rotate ? double(ms) : 1.0) * 1.4426950408889634);
+    p.c_log2 = float(scale * double(ms) * 1.4426950408889634);
     p.ctas = decode_ctas();
     p.part_o = static_cast<float *>(workspace);
     p.part_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) +

@@ -39,6 +39,7 @@ struct VarlenParams {
     int rotate_q, half;
     float c_log2;                           // logit scale in log2 units
     unsigned long long timeout_ns;
+    float ms;                               // the mode's attention scale (1: not rotated)
     double theta[64];
 };
 

@@ -359,13 +359,13 @@ def paged_decode(cache, q, seq_ids, rope: RopeParams, layer: int = 0, window: in
     if o.shape != q.shape:
         raise ValueError("out must be shaped like q")
     if return_lse and lse is None:
-        lse = torch.empty((n, Hq), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((n, Hq), dtype=torch.float32)
     if lse is not None and (lse.shape != (n, Hq) or lse.dtype != torch.float32 or
                             not lse.is_contiguous()):
         raise ValueError("lse must be contiguous fp32 [%d, %d]" % (n, Hq))
     if workspace is None and Hq % cache.kv_heads == 0:
         need = paged_decode_workspace_bytes(cache, n, Hq)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(max(need, 1), dtype=torch.uint8)
     rope_c = _rope_c(rope)      # (alive during the call: it owns factor tables)
     a = _DecodeArgs(q.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(), ids, word,
                     n, Hq, int(layer), _strides3(q), _strides3(o), rope_c, int(window),

@@ -131,20 +131,20 @@ def attn_varlen(q, k, v, plan: VarlenPlan, rope: RopeParams, causal: bool = True
         raise ValueError("q, k, v must share a dtype")
     _same_device(q, k=k, v=v, out=out, lse=lse, workspace=workspace, status=status,
                  plan=plan.plan)
-    alloc = torch.empty if plan.total_q == Tq else torch.zeros
-    o = out if out is not None else alloc((Tq, Hq, D), dtype=q.dtype, device=q.device)
+    alloc = q.new_empty if plan.total_q == Tq else q.new_zeros
+    o = out if out is not None else alloc((Tq, Hq, D))
     if o.shape != q.shape or o.dtype != q.dtype:
         raise ValueError("out must be shaped like q")
     if return_lse and lse is None:
-        lse = alloc((Hq, Tq), dtype=torch.float32, device=q.device)
+        lse = alloc((Hq, Tq), dtype=torch.float32)
     if lse is not None and (lse.shape != (Hq, Tq) or lse.dtype != torch.float32 or
                             not lse.is_contiguous()):
         raise ValueError("lse must be contiguous fp32 [%d, %d]" % (Hq, Tq))
     if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
         raise ValueError("status must be an int32 tensor")
     if workspace is None and not prerotated and rope.mode != "none":
-        workspace = torch.empty(max(varlen_workspace_bytes(plan, Hkv, D, k.dtype), 1),
-                                dtype=torch.uint8, device=k.device)
+        workspace = k.new_empty(max(varlen_workspace_bytes(plan, Hkv, D, k.dtype), 1),
+                                dtype=torch.uint8)
     ws, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
     rope_c = _rope_c(rope)      # (alive during the call: it owns factor tables)
     a = _VarlenArgs(
