@@ -85,13 +85,6 @@ struct F32 {
     static constexpr int kBytes = ((kRows + 2 * kKeys) * D + kRows * kKeys) * 4;
 };
 
-// x in two tf32 parts, both cut (the matrix instruction reads a value's first 19 bits).
-// A NaN or infinite x has a NaN part: its products are NaN.
-__device__ __forceinline__ void tf32_parts(float x, uint32_t &hi, uint32_t &lo) {
-    hi = __float_as_uint(x) & 0xffffe000u;
-    lo = __float_as_uint(x - __uint_as_float(hi));
-}
-
 // Float offset of chunk c of row r: rows of Q and K are read two at a time, four
 // chunks each, rows of V in pairs, four pairs by two chunks, without bank conflicts.
 template <int D>

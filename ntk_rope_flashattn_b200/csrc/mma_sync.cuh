@@ -24,6 +24,14 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// x in two tf32 parts, both cut, not rounded (two cheap instructions; the matrix
+// instruction reads a value's first 19 bits): x - hi is exact and lo counts with its
+// first 11 bits, so hi + lo is within 2^-21 of x.  A NaN or infinite x has a NaN part.
+__device__ __forceinline__ void tf32_parts(float x, uint32_t &hi, uint32_t &lo) {
+    hi = __float_as_uint(x) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
+}
+
 // Four 8 x 8 blocks of 16-bit values; lane l gives the address of row l % 8 of
 // block l / 8.
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {

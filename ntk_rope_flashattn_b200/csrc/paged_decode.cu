@@ -182,14 +182,12 @@ __device__ __forceinline__ uint32_t row_at(uint32_t at, int rows, bool value) {
     return (at ^ (x << 4)) + rows * CPR * 16;
 }
 
-// x in two tf32 parts, both cut (not rounded: three cheap instructions instead of
-// two conversions): x - hi is exact, lo keeps its first 11 bits, so hi + lo is
-// within 2^-21 of x.  An infinite x has no second part.
+// tf32_parts of a factor whose products are not summed apart: an infinite x has no
+// second part, so that its products stay infinite.
 __device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
-    hi = __float_as_uint(x) & 0xffffe000u;
-    float l = x - __uint_as_float(hi);
-    l = l == l ? l : 0.f;
-    lo = __float_as_uint(l) & 0xffffe000u;
+    tf32_parts(x, hi, lo);
+    const float l = __uint_as_float(lo);
+    lo = l == l ? lo : 0;
 }
 // Two values in two bf16 parts each, packed.
 __device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint32_t &lo) {
@@ -539,10 +537,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                                        j * 8 * C::ROW)
                                  : "memory");
                     uint32_t h[4], w[4];
-                    split_tf32(x.x, h[0], w[0]);
-                    split_tf32(x.y, h[1], w[1]);
-                    split_tf32(x.z, h[2], w[2]);
-                    split_tf32(x.w, h[3], w[3]);
+                    tf32_parts(x.x, h[0], w[0]);
+                    tf32_parts(x.y, h[1], w[1]);
+                    tf32_parts(x.z, h[2], w[2]);
+                    tf32_parts(x.w, h[3], w[3]);
                     mma_tf32(low, qf[2 * i], w[0], w[1]);
                     mma_tf32(low2, qf[2 * i + 1], w[2], w[3]);
                     mma_tf32(s[j], qf[2 * i], h[0], h[1]);
@@ -642,8 +640,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int j = 0; j < NS; ++j) {
                 // k slots c4 and c4 + 4 hold keys 2 c4 and 2 c4 + 1
                 uint32_t a[4];
-                split_tf32(s[j][0], a[0], a[1]);
-                split_tf32(s[j][1], a[2], a[3]);
+                tf32_parts(s[j][0], a[0], a[1]);
+                tf32_parts(s[j][1], a[2], a[3]);
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
                     // columns 32 i + 4 g + {0..3}: one per output tile 4 i + {0..3}
