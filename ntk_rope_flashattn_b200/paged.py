@@ -18,6 +18,7 @@ page) skips the entry and is reported through the optional ``status`` tensor
 """
 import ctypes
 import functools
+import struct
 
 from . import RopeParams, _check, _dtype_code, _RopeParams, _same_device, load
 
@@ -49,6 +50,38 @@ class _DecodeArgs(ctypes.Structure):
                 ("n", _I64), ("Hq", _I64), ("layer", _I64), ("q_strides", _I64 * 3),
                 ("o_strides", _I64 * 3), ("rope", _RopeParams), ("window", _I64),
                 ("sinks", _I64), ("softmax_scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+_CODES = {_P: "P", _I64: "q", _I32: "i", ctypes.c_uint32: "I", ctypes.c_float: "f"}
+
+
+def _packer(cls):
+    """pack(*values) -> the bytes of a cls (three times as fast as filling one): arrays
+    spread, a NULL as 0, structs inside as bytes."""
+    fmt = ""
+    for _, t in cls._fields_:
+        if issubclass(t, ctypes.Array):
+            fmt += "%d%s" % (t._length_, _CODES[t._type_])
+        elif issubclass(t, ctypes.Structure):
+            fmt += "%ds" % ctypes.sizeof(t)
+        else:
+            fmt += _CODES[t]
+    s = struct.Struct("@" + fmt + "0q")
+    assert s.size == ctypes.sizeof(cls)
+    return s.pack
+
+
+_pack_append, _pack_decode = _packer(_AppendArgs), _packer(_DecodeArgs)
+
+
+@functools.lru_cache(maxsize=None)
+def _raw(name, pointers, sizes=0):
+    """The entry point under argument types that take packed structs: `pointers`
+    addresses (or bytes), `sizes` int64 values, the stream."""
+    fn = load()[name]
+    fn.argtypes = [_P] * pointers + [_I64] * sizes + [_P]
+    fn.restype = ctypes.c_int
+    return fn
 
 
 def _declare(lib):
@@ -165,7 +198,7 @@ def _index(cache, **tensors):
     out = []
     for name, t in tensors.items():
         if t is None:
-            out.append(None)
+            out.append(0)
             continue
         if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1:
             raise ValueError("%s must be a 1-D int32 tensor" % name)
@@ -245,23 +278,18 @@ def _tokens(t, name, heads, D, dtype):
         raise ValueError("%s must be %s" % (name, dtype))
 
 
-_Strides3 = _I64 * 3
-
-
-def _strides3(t):
-    return _Strides3(*t.stride())
-
-
 @functools.lru_cache(maxsize=64)
 def _rope_struct(*fields):
-    return RopeParams(*fields)._c()
+    c = RopeParams(*fields)._c()
+    return c, bytes(c)
 
 
 def _rope_c(rope):
-    """The rope's C struct, one per set of field values (factor tables may change in
-    place: built anew)."""
+    """The rope's C struct and its bytes, one per set of field values (factor tables may
+    change in place: built anew; the struct keeps the arrays that the bytes point to)."""
     if rope.factors is not None or rope.factors_short is not None:
-        return rope._c()
+        c = rope._c()
+        return c, bytes(c)
     return _rope_struct(rope.mode, int(rope.head_dim), float(rope.base), float(rope.scale),
                         int(rope.original_max_pos), float(rope.alpha), float(rope.beta),
                         rope.pairing, int(rope.seq_len))
@@ -309,15 +337,15 @@ def paged_append(cache, k, v, seq_ids, start, rope: RopeParams, layer: int = 0, 
         _tokens(k_out, "k_out", H, D, cache.dtype)
         if k_out.shape != k.shape:
             raise ValueError("k_out must be shaped like k")
-    none = _Strides3()
-    rope_c = _rope_c(rope)      # (alive during the call: it owns factor tables)
-    a = _AppendArgs(
-        k.data_ptr(), v.data_ptr(), None if q is None else q.data_ptr(),
-        None if q is None else q_out.data_ptr(), None if k_out is None else k_out.data_ptr(), ids,
-        st, cu, word, seq_ids.shape[0], T, Hq, int(layer), _strides3(k), _strides3(v),
-        none if q is None else _strides3(q), none if q is None else _strides3(q_out),
-        none if k_out is None else _strides3(k_out), rope_c)
-    _launch(cache, load().lcx_paged_append, cache._struct, ctypes.byref(a))
+    none = (0, 0, 0)
+    owner, rope_c = _rope_c(rope)      # (alive during the call: it owns factor tables)
+    a = _pack_append(
+        k.data_ptr(), v.data_ptr(), 0 if q is None else q.data_ptr(),
+        0 if q is None else q_out.data_ptr(), 0 if k_out is None else k_out.data_ptr(), ids, st,
+        cu, word, seq_ids.shape[0], T, Hq, int(layer), *k.stride(), *v.stride(),
+        *(none if q is None else q.stride()), *(none if q is None else q_out.stride()),
+        *(none if k_out is None else k_out.stride()), rope_c)
+    _launch(cache, _raw("lcx_paged_append", 2), cache._struct, a)
     return q_out
 
 
@@ -366,10 +394,10 @@ def paged_decode(cache, q, seq_ids, rope: RopeParams, layer: int = 0, window: in
     if workspace is None and Hq % cache.kv_heads == 0:
         need = paged_decode_workspace_bytes(cache, n, Hq)
         workspace = q.new_empty(max(need, 1), dtype=torch.uint8)
-    rope_c = _rope_c(rope)      # (alive during the call: it owns factor tables)
-    a = _DecodeArgs(q.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(), ids, word,
-                    n, Hq, int(layer), _strides3(q), _strides3(o), rope_c, int(window),
-                    int(sinks), float(softmax_scale), LCX_DECODE_PREROTATED if prerotated else 0)
+    owner, rope_c = _rope_c(rope)      # (alive during the call: it owns factor tables)
+    a = _pack_decode(q.data_ptr(), o.data_ptr(), 0 if lse is None else lse.data_ptr(), ids, word,
+                     n, Hq, int(layer), *q.stride(), *o.stride(), rope_c, int(window), int(sinks),
+                     float(softmax_scale), LCX_DECODE_PREROTATED if prerotated else 0)
     ws, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-    _launch(cache, load().lcx_paged_decode, cache._struct, ctypes.byref(a), ws, size)
+    _launch(cache, _raw("lcx_paged_decode", 3, 1), cache._struct, a, ws, size)
     return (o, lse) if return_lse else o

@@ -9,7 +9,7 @@ import ctypes
 import numpy as np
 
 from . import RopeParams, _check, _dtype_code, _RopeParams, _same_device, load
-from .paged import _call_on, _rope_c, _strides3
+from .paged import _call_on, _packer, _raw, _rope_c
 
 LCX_VARLEN_PREROTATED = 1
 LCX_VARLEN_TEST_STALL = 0x80000000
@@ -30,6 +30,9 @@ class _VarlenArgs(ctypes.Structure):
                 ("v_strides", _I64 * 3), ("o_strides", _I64 * 3), ("rope", _RopeParams),
                 ("window", _I64), ("sinks", _I64), ("softmax_scale", ctypes.c_float),
                 ("flags", ctypes.c_uint32), ("watchdog_ms", _I32), ("reserved0", _I32)]
+
+
+_pack_args = _packer(_VarlenArgs)
 
 
 def _declare(lib):
@@ -70,6 +73,7 @@ class VarlenPlan:
         host = torch.zeros(ints, dtype=torch.int32)
         self.info = _Info()
         _check(load().lcx_varlen_plan(pq, pk, n, host.data_ptr(), ints, ctypes.byref(self.info)))
+        self._info_bytes = bytes(self.info)
         self.device = device
         self.plan = host.to(device)
         self.total_q, self.total_k = int(self.info.total_q), int(self.info.total_k)
@@ -145,15 +149,15 @@ def attn_varlen(q, k, v, plan: VarlenPlan, rope: RopeParams, causal: bool = True
     if workspace is None and not prerotated and rope.mode != "none":
         workspace = k.new_empty(max(varlen_workspace_bytes(plan, Hkv, D, k.dtype), 1),
                                 dtype=torch.uint8)
-    ws, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-    rope_c = _rope_c(rope)      # (alive during the call: it owns factor tables)
-    a = _VarlenArgs(
+    ws, size = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    owner, rope_c = _rope_c(rope)      # (alive during the call: it owns factor tables)
+    a = _pack_args(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-        None if lse is None else lse.data_ptr(), plan.plan.data_ptr(), ws, size,
-        None if status is None else status.data_ptr(), plan.info, _dtype_code(q),
-        1 if causal else 0, Tq, Tk, Hq, Hkv, D, _strides3(q), _strides3(k), _strides3(v),
-        _strides3(o), rope_c, int(window), int(sinks), float(softmax_scale),
+        0 if lse is None else lse.data_ptr(), plan.plan.data_ptr(), ws, size,
+        0 if status is None else status.data_ptr(), plan._info_bytes, _dtype_code(q),
+        1 if causal else 0, Tq, Tk, Hq, Hkv, D, *q.stride(), *k.stride(), *v.stride(),
+        *o.stride(), rope_c, int(window), int(sinks), float(softmax_scale),
         (LCX_VARLEN_PREROTATED if prerotated else 0) |
         (LCX_VARLEN_TEST_STALL if _test_stall else 0), int(watchdog_ms), 0)
-    _call_on(q.device.index, load().lcx_attn_varlen, ctypes.byref(a))
+    _call_on(q.device.index, _raw("lcx_attn_varlen", 1), a)
     return (o, lse) if return_lse else o

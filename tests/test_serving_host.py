@@ -292,13 +292,29 @@ def test_rope_struct_follows_the_fields():
     import copy
     import pickle
     r = rope(mode="yarn", scale=4.0)
-    a = paged._rope_c(r)
-    assert bytes(a) == bytes(r._c()) and paged._rope_c(r) is a
+    a, packed = paged._rope_c(r)
+    assert bytes(a) == packed == bytes(r._c()) and paged._rope_c(r)[0] is a
     assert pickle.loads(pickle.dumps(r)) == r == copy.deepcopy(r)
     r.scale = 8.0
-    assert bytes(paged._rope_c(r)) == bytes(r._c()) != bytes(a)
+    assert paged._rope_c(r)[1] == bytes(r._c()) != packed
     f = rope(mode="factors", factors=np.ones(64))
-    assert paged._rope_c(f) is not paged._rope_c(f)
+    assert paged._rope_c(f)[0] is not paged._rope_c(f)[0]
+
+
+def test_packed_structs_are_the_declared_ones():
+    r = rope(mode="yarn", scale=4.0)._c()
+    s = (ctypes.c_int64 * 3)(11, 12, 13)
+    want = paged._DecodeArgs(1, 2, None, 4, None, 6, 7, 8, s, s, r, 9, 10, 0.5, 1)
+    assert paged._pack_decode(1, 2, 0, 4, 0, 6, 7, 8, *s, *s, bytes(r), 9, 10, 0.5, 1) == bytes(want)
+    want = paged._AppendArgs(1, 2, 3, 4, None, 6, 7, 8, 9, 10, 11, 12, 13, s, s, s, s, s, r)
+    got = paged._pack_append(1, 2, 3, 4, 0, 6, 7, 8, 9, 10, 11, 12, 13, *s, *s, *s, *s, *s, bytes(r))
+    assert got == bytes(want)
+    info = lcx.VarlenPlan([3, 5], device="cpu").info
+    want = varlen._VarlenArgs(1, 2, 3, 4, 5, 6, 7, 8, 9, info, 0, 1, 12, 13, 14, 15, 16, s, s, s, s,
+                              r, 17, 18, 0.25, 1, 20, 0)
+    got = varlen._pack_args(1, 2, 3, 4, 5, 6, 7, 8, 9, bytes(info), 0, 1, 12, 13, 14, 15, 16, *s, *s,
+                            *s, *s, bytes(r), 17, 18, 0.25, 1, 20, 0)
+    assert got == bytes(want)
 
 
 def test_binding_refuses_host_tensors():
