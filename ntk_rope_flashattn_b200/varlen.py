@@ -60,9 +60,9 @@ class VarlenPlan:
         for x in (seqlens_q, seqlens_q if seqlens_k is None else seqlens_k):
             if isinstance(x, torch.Tensor) and x.is_cuda:
                 raise ValueError("sequence lengths are host integers (got a CUDA tensor)")
-            a = np.asarray(x, dtype=np.int64).reshape(-1)
-            if a.size and (a.min() < 0 or a.max() > 2 ** 30):
-                raise ValueError("sequence lengths must be in [0, 2^30]")
+            a = np.asarray(x).reshape(-1)
+            if a.size and (a.dtype.kind not in "iu" or a.min() < 0 or a.max() > 2 ** 30):
+                raise ValueError("sequence lengths must be integers in [0, 2^30]")
             lens.append(np.ascontiguousarray(a, np.int32))
         if lens[0].size != lens[1].size:
             raise ValueError("seqlens_q and seqlens_k must have the same length")

@@ -83,6 +83,20 @@ def test_plan_covers_every_row_once(lq, lk):
         assert seen == set(range(sum(lq)))
 
 
+@pytest.mark.parametrize("lens", [[1.5], [2.0, 3.0], ["4"], [True], [1 << 40]])
+def test_plan_takes_whole_numbers(lens):
+    with pytest.raises(ValueError):
+        lcx.VarlenPlan(lens, device="cpu")
+
+
+def test_plan_of_arrays():
+    """Lists, arrays and host tensors of any integer type make the same plan."""
+    a = lcx.VarlenPlan([5, 0, 300], device="cpu").plan
+    for x in (np.array([5, 0, 300], np.uint16), torch.tensor([5, 0, 300]), (5, 0, 300)):
+        assert torch.equal(lcx.VarlenPlan(x, device="cpu").plan, a)
+    assert lcx.VarlenPlan([], device="cpu").total_q == 0
+
+
 def test_plan_refusals(lib):
     with pytest.raises(ValueError):
         lcx.VarlenPlan([-1], device="cpu")
