@@ -446,6 +446,14 @@ __device__ __forceinline__ float abs_max8(const float (&x)[8]) {
     return fmaxf(a, b);
 }
 
+// The same of 8 packed fp16 values.
+__device__ __forceinline__ float packed_max(const uint4 &h) {
+    const __half2 *v = reinterpret_cast<const __half2 *>(&h);
+    const __half2 a = __hmax2(__hmax2(__habs2(v[0]), __habs2(v[1])),
+                              __hmax2(__habs2(v[2]), __habs2(v[3])));
+    return fmaxf(__low2float(a), __high2float(a));
+}
+
 // Rotate the pairs of one job: HALF pairs x1[e], x2[e] with angle e; else adjacent
 // pairs of x1 with angle e (x2 unused).
 template <bool kHalf>
@@ -647,7 +655,8 @@ struct Bars {
     int border_tile[kMaxBorder];
     uint32_t bad[kMaxBorder][4];    // rows of a border tile with non-finite values
     signed char q_exp[2 * kBM];     // exponents of the query rows' scales
-    // per pair, for the query rotation (lanes read different entries, which the
+    // per pair (pair e of job q at e CPR + q: a warp's lanes read neighbours), for the
+    // query rotation (lanes read different entries, which the
     // parameter space would serve one after the other): the angle of the block's first
     // position reduced to [-pi, pi], theta in two fp32 parts, cos and sin of the step
     float base[D / 2];
@@ -742,16 +751,16 @@ __device__ __forceinline__ void rotate_queries(const Block &b, int tid, uint8_t 
         // The row's angle r0 theta (r0 < 96) on top of the block's: 2 pi in two parts, the
         // first of 16 bits so that its multiples are exact; within 2^-22 in all.  (The
         // fp64 reduction per thread took 2.3k cycles of the 384 threads.)
-        const float2 th = bar.theta[q * J::PPJ + e];
+        const float2 th = bar.theta[e * J::CPR + q];
         const float r = static_cast<float>(r0);
         const float k = rintf(r * th.x * 0.15915494f);
         float a = fmaf(r, th.x, -k * 6.28314208984375f);
         a = fmaf(k, -4.32173358e-5f, a);
-        a = fmaf(r, th.y, a) + bar.base[q * J::PPJ + e];
+        a = fmaf(r, th.y, a) + bar.base[e * J::CPR + q];
         const float k2 = rintf(a * 0.15915494f);
         a = fmaf(k2, -4.32173358e-5f, fmaf(k2, -6.28314208984375f, a));
         __sincosf(a, &s[e], &c[e]);
-        st[e] = bar.step[q * J::PPJ + e];
+        st[e] = bar.step[e * J::CPR + q];
     }
     ok = __all_sync(0xffffffffu, mbar_wait(&bar.full_q, 0, abort, tmo));
     if (!ok) return;
@@ -771,28 +780,35 @@ __device__ __forceinline__ void rotate_queries(const Block &b, int tid, uint8_t 
                 va[x] = *reinterpret_cast<const uint4 *>(from + oa);
                 if constexpr (kHalf) vb[x] = *reinterpret_cast<const uint4 *>(from + ob);
             }
-            float mx[2];
+            uint4 h1[2], h2[2];
+            bool in = true;                // the largest value of the job is in range
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 unpack(va[x], x1[x]);
                 if constexpr (kHalf) unpack(vb[x], x2[x]);
                 turn<kHalf>(x1[x], x2[x], c, s);
-                mx[x] = kHalf ? fmaxf(abs_max8(x1[x]), abs_max8(x2[x])) : abs_max8(x1[x]);
+                h1[x] = half_parts(x1[x]);
+                float mx = packed_max(h1[x]);
+                if constexpr (kHalf) {
+                    h2[x] = half_parts(x2[x]);
+                    mx = fmaxf(mx, packed_max(h2[x]));
+                }
+                in = in && mx >= 0.015625f && mx < 16384.f;
             }
             int ex[2] = {0, 0};
             // (rows, and the rows of a pass, are whole warps': the warp is together here)
             // without a value out of range in any lane no row maximum is needed
             constexpr uint32_t lanes = 0xffffffffu;
-            const bool in = mx[0] >= 0.015625f && mx[0] < 16384.f && mx[1] >= 0.015625f &&
-                            mx[1] < 16384.f;
             if (__any_sync(lanes, !in)) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
+                    float mx = abs_max8(x1[x]);
+                    if constexpr (kHalf) mx = fmaxf(mx, abs_max8(x2[x]));
 #pragma unroll
                     for (int o = 1; o < J::CPR; o <<= 1)
-                        mx[x] = fmaxf(mx[x], __shfl_xor_sync(lanes, mx[x], o));
+                        mx = fmaxf(mx, __shfl_xor_sync(lanes, mx, o));
                     float undo;
-                    const float f = range_scale(mx[x], &undo);
+                    const float f = range_scale(mx, &undo);
                     ex[x] = int(__float_as_uint(undo) >> 23) - 127;
                     if (ex[x]) {
 #pragma unroll
@@ -800,6 +816,8 @@ __device__ __forceinline__ void rotate_queries(const Block &b, int tid, uint8_t 
                             x1[x][e] *= f;
                             if constexpr (kHalf) x2[x][e] *= f;
                         }
+                        h1[x] = half_parts(x1[x]);
+                        if constexpr (kHalf) h2[x] = half_parts(x2[x]);
                     }
                 }
             }
@@ -809,13 +827,11 @@ __device__ __forceinline__ void rotate_queries(const Block &b, int tid, uint8_t 
                 uint8_t *to = tile + x * Tc<D>::kTile;
                 uint8_t *low = to + Tc<D>::kOffQLo;
                 if (q == 0) bar.q_exp[(t0 + x) * kBM + r] = (signed char)ex[x];
-                const uint4 h1 = half_parts(x1[x]);
-                *reinterpret_cast<uint4 *>(to + oa) = h1;
-                if (b.precise) *reinterpret_cast<uint4 *>(low + oa) = half_rest(x1[x], h1);
+                *reinterpret_cast<uint4 *>(to + oa) = h1[x];
+                if (b.precise) *reinterpret_cast<uint4 *>(low + oa) = half_rest(x1[x], h1[x]);
                 if constexpr (kHalf) {
-                    const uint4 h2 = half_parts(x2[x]);
-                    *reinterpret_cast<uint4 *>(to + ob) = h2;
-                    if (b.precise) *reinterpret_cast<uint4 *>(low + ob) = half_rest(x2[x], h2);
+                    *reinterpret_cast<uint4 *>(to + ob) = h2[x];
+                    if (b.precise) *reinterpret_cast<uint4 *>(low + ob) = half_rest(x2[x], h2[x]);
                 }
             }
 #pragma unroll
@@ -931,13 +947,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 b0.u.q0 + t * b0.rstep, b0.h0 + t * b0.hstep, 0);
         }
     }
+    // (the work before the first barrier is spread over the warps: every CTA waits for it)
     if (p.fp16 && threadIdx.x >= 128 && threadIdx.x < 128 + D / 2) {
         const int i = threadIdx.x - 128;
+        using J = Job<D, kHalf>;
+        const int at = i % J::PPJ * J::CPR + i / J::PPJ;
         const double th = v.theta[i];
         const float hi = static_cast<float>(th);
-        bar.base[i] = rope_reduced_angle((long long)b0.u.pos0, th);
-        bar.theta[i] = make_float2(hi, static_cast<float>(th - hi));
-        bar.step[i] = p.step[i];
+        bar.base[at] = rope_reduced_angle((long long)b0.u.pos0, th);
+        bar.theta[at] = make_float2(hi, static_cast<float>(th - hi));
+        bar.step[at] = p.step[i];
     }
     if (threadIdx.x == 0) {
         mbar_init(&bar.ready_q, kRotThreads + 1);
@@ -1267,16 +1286,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool wide =
                     !((reinterpret_cast<uintptr_t>(v.o) | (v.os[0] * 2) | (v.os[1] * 2)) & 31);
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    float o[32];
+                for (int c = 0; c < D / 64; ++c) {
+                    float o[64];
                     if (n > 0) {
-                        tmem_ld32(trow + o_col + c * 32, o);
+                        tmem_ld64(trow + o_col + c * 64, o);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                        for (int e = 0; e < 64; ++e) o[e] = 0.f;
                     }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] *= inv;
+                    for (int e = 0; e < 64; ++e) o[e] *= inv;
                     if (bad && valid) {
                         // non-finite values of border tiles that this row does see
                         for (int i = 0; i < nb; ++i) {
@@ -1290,9 +1309,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     continue;
                                 const __nv_bfloat16 *src =
                                     reinterpret_cast<const __nv_bfloat16 *>(v.v) +
-                                    (long long)(B.u.k0 + key) * v.vs[0] + B.g * v.vs[1] + c * 32;
+                                    (long long)(B.u.k0 + key) * v.vs[0] + B.g * v.vs[1] + c * 64;
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) {
+                                for (int e = 0; e < 64; ++e) {
                                     const float y = static_cast<float>(src[e]);
                                     if (!(fabsf(y) < INFINITY)) o[e] += y;
                                 }
@@ -1300,8 +1319,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        *reinterpret_cast<uint4 *>(stage + (((c * 4 + e) ^ (row & 7)) << 4)) =
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<uint4 *>(stage + (((c * 8 + e) ^ (row & 7)) << 4)) =
                             make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]),
                                        pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
                                        pack_bf16x2(o[8 * e + 4], o[8 * e + 5]),
