@@ -395,7 +395,7 @@ lcx_status launch_f32(const VarlenParams &p, bool after_keys, cudaStream_t s) {
 
 // ------------------------------------------------------------------ key rotation
 // The rotated keys as the tcgen05 kernel reads them: fp16 parts hi [T][Hkv][D],
-// remainders lo alike (rows before kLoRows, all of them with kAllLo), one scale per
+// remainders lo alike (rows before kLoRows, all of them with all_lo), one scale per
 // row (k' = scale (hi + lo)), and per CTA whether any scale is not 1.
 constexpr int kLoRows = 384;   // a precise block's keys: positions below 127 + 256
 
@@ -494,6 +494,7 @@ __global__ void __launch_bounds__(kKeyThreads)
     constexpr int RPC = kKeyThreads / J::CPR;            // tokens per CTA
     __shared__ int pos_of[RPC];
     __shared__ int scaled;
+    wait_previous_kernel();
     pdl_launch_dependents();
     const int t0 = blockIdx.x * RPC;
     if (threadIdx.x == 0) scaled = 0;
@@ -1430,8 +1431,10 @@ KeySpace key_space(int64_t total_k, int64_t H, int64_t D, int dtype) {
 template <int D, bool kHalf>
 lcx_status launch_keys(KeyParams &k, cudaStream_t s) {
     constexpr int rpc = kKeyThreads / Job<D, kHalf>::CPR;
-    varlen_keys_kernel<D, kHalf><<<unsigned((k.T + rpc - 1) / rpc), kKeyThreads, 0, s>>>(k);
-    const cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_dependent(varlen_keys_kernel<D, kHalf>,
+                                     dim3(unsigned((k.T + rpc - 1) / rpc)), dim3(kKeyThreads), 0,
+                                     s, k);
+    if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess)
         return fail(LCX_ERR_CUDA, "attn_varlen key launch failed: %s", cudaGetErrorString(e));
     return LCX_OK;
@@ -1737,7 +1740,7 @@ extern "C" lcx_status lcx_attn_varlen(const lcx_varlen_args *a, void *stream) {
     if (a->dtype == LCX_BF16) return run_tc(a, p, s);
     if (p.rotate_q) {
         st = rotate_packed(&a->rope, std::max<int64_t>(a->info.max_k, 1), a->k, a->k_strides,
-                           a->workspace, a->dtype, a->plan + plan_cu_k(a->info.n_seqs),
+                           a->workspace, a->plan + plan_cu_k(a->info.n_seqs),
                            int(a->info.n_seqs), a->info.total_k, a->Hkv, a->D, s);
         if (st != LCX_OK) return st;
     }

@@ -62,11 +62,11 @@ lcx_status launch_merge(const float *o_parts, const float *lse_parts, int n_part
 // length for the length-dependent modes (rope.seq_len, or seq_len when > 0).
 lcx_status check_serving_rope(const lcx_rope_params *r, int64_t D, int64_t seq_len);
 
-// Rotate packed keys x [T, H, D] (strides: token, head) into contiguous y, the
+// Rotate packed fp32 keys x [T, H, D] (strides: token, head) into contiguous y, the
 // positions of sequence i's rows cu[i] .. cu[i + 1] - 1 counted from 0 (cu:
 // device).  Arguments are assumed valid.
 lcx_status rotate_packed(const lcx_rope_params *rope, int64_t seq_len, const void *x,
-                         const int64_t *x_strides, void *y, int dtype, const int *cu, int n,
+                         const int64_t *x_strides, void *y, const int *cu, int n,
                          int64_t T, int64_t H, int64_t D, cudaStream_t s);
 
 }  // namespace lcx

@@ -52,7 +52,9 @@ lcx_status check_distinct(const int64_t *st, int64_t tokens, int64_t heads, cons
 
 // Launch `kern` as a programmatic dependent of the stream's previous kernel: it
 // may be scheduled while that one ends and waits (griddepcontrol.wait) for its
-// results.
+// results.  A call's first kernel waits before all else and in every CTA, so that
+// what it lets start early (pdl_launch_dependents) and what follows it find the
+// stream's earlier work done.
 template <typename... Params, typename... Args>
 cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem,
                              cudaStream_t s, Args... args) {

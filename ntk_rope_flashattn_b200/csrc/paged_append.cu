@@ -1,5 +1,5 @@
 // paged_append.cu -- rotate new tokens' keys and queries and write keys and
-// values into cache pages (lcx_paged_append); also the rotate pass of packed
+// values into cache pages (lcx_paged_append); also the rotate pass of packed fp32
 // keys that lcx_attn_varlen runs first.
 //
 // y_p = ms (x_p cos phi - x_q sin phi), y_q = ms (x_p sin phi + x_q cos phi),
@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     constexpr int N = Vec<T>::N;
     constexpr int NP = kHalf ? N : N / 2;           // pairs per job
     __shared__ Place place[kThreads];
+    wait_previous_kernel();
     pdl_launch_dependents();       // attention over packed fp32 rows may be scheduled
     const int t0 = blockIdx.x * a.rows;
     const int job = threadIdx.x % a.jobs, row = threadIdx.x / a.jobs, t = t0 + row;
@@ -207,21 +208,18 @@ lcx_status launch_append(AppendParams &a, int es, bool half, cudaStream_t s) {
     const int heads = a.Hkv + (a.v.p ? a.Hkv : 0) + (a.q.p ? a.Hq : 0);
     // Many tokens: a CTA of as many tokens as its threads hold walks all heads, the
     // angles evaluated once per token.  Few tokens (a decode step): the heads are cut
-    // into slices of at least four until there are about eight CTAs per SM; the angles are evaluated once per slice, which costs
-    // less than the walk (64 tokens, 48 heads: 18.3 us walked, 6.5 us in slices).
+    // into slices of at least four until there are about eight CTAs per SM; the angles are
+    // evaluated once per slice, which costs less than the walk (64 tokens, 48 heads: 18.3 us walked, 6.5 us in slices).
     const long long ctas = (a.T + a.rows - 1) / a.rows;
     const long long want = std::max<long long>(1, 8ll * device_sms() / ctas);
     a.per = int((heads + want - 1) / want);
     a.per = std::min(heads, std::max(4, (a.per + 3) / 4 * 4));
     a.slices = (heads + a.per - 1) / a.per;
     const dim3 grid{unsigned(ctas), unsigned(a.slices)};
-    if (es == 2)
-        half ? append_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, s>>>(a)
-             : append_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, s>>>(a);
-    else
-        half ? append_kernel<float, true><<<grid, kThreads, 0, s>>>(a)
-             : append_kernel<float, false><<<grid, kThreads, 0, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    auto kern = es == 2 ? (half ? append_kernel<__nv_bfloat16, true> : append_kernel<__nv_bfloat16, false>)
+                        : (half ? append_kernel<float, true> : append_kernel<float, false>);
+    cudaError_t e = launch_dependent(kern, grid, dim3(kThreads), 0, s, a);
+    if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess)
         return fail(LCX_ERR_CUDA, "paged_append launch failed: %s", cudaGetErrorString(e));
     return LCX_OK;
@@ -243,7 +241,7 @@ lcx_status check_serving_rope(const lcx_rope_params *r, int64_t D, int64_t seq_l
 }
 
 lcx_status rotate_packed(const lcx_rope_params *rope, int64_t seq_len, const void *x,
-                         const int64_t *x_strides, void *y, int dtype, const int *cu, int n,
+                         const int64_t *x_strides, void *y, const int *cu, int n,
                          int64_t T, int64_t H, int64_t D, cudaStream_t s) {
     if (T == 0) return LCX_OK;
     AppendParams a = {};
@@ -255,7 +253,7 @@ lcx_status rotate_packed(const lcx_rope_params *rope, int64_t seq_len, const voi
     a.Hkv = int(H);
     a.D = int(D);
     rope_freqs_unchecked(rope, effective_seq_len(rope, seq_len), a.theta, &a.ms);
-    return launch_append(a, dtype == LCX_BF16 ? 2 : 4, rope->pairing == LCX_PAIR_HALF, s);
+    return launch_append(a, 4, rope->pairing == LCX_PAIR_HALF, s);
 }
 
 }  // namespace lcx

@@ -212,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     float *sO = reinterpret_cast<float *>(sm + C::kOffO);     // [warp][8][64]
     float *sM = reinterpret_cast<float *>(sm + C::kOffM);     // [warp][16][2]
     const int R = p.Hkv * p.hb;
+    wait_previous_kernel();
     pdl_launch_dependents();   // the join may be scheduled; it waits for this grid
 
     // This CTA's stretch [b0, b1) of the block list, and the entry that holds b0:
@@ -930,8 +931,8 @@ lcx_status launch_decode(DecodeParams &p, cudaStream_t s) {
     if (most * p.n > 0x7fffffffLL)
         return fail(LCX_ERR_UNSUPPORTED, "too many entries for sequences of this length");
     p.ctas = int(std::min<long long>(p.ctas, segments * most));
-    kern<<<unsigned(p.ctas), kThreads, C::kSmem, s>>>(p);
-    if ((e = cudaGetLastError()) == cudaSuccess && p.ctas > 1)
+    e = launch_dependent(kern, dim3(unsigned(p.ctas)), dim3(kThreads), C::kSmem, s, p);
+    if (e == cudaSuccess && p.ctas > 1)
         e = launch_dependent(join_kernel<T, D, C::HB>, dim3(unsigned(segments)), dim3(kThreads), 0,
                              s, p);
     if (e == cudaSuccess) e = cudaGetLastError();

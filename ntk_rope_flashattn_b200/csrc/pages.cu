@@ -63,6 +63,7 @@ __device__ int free_depth(const PagedParams &p) { return min(max(*p.n_free, 0), 
 __global__ void __launch_bounds__(kT)
     extend_kernel(const __grid_constant__ PagedParams p, const int *ids, const int *n_new, int n,
                   int *start, int *status) {
+    wait_previous_kernel();
     __shared__ int s_id[kT], s_end[kT], s_first[kT];
     const int i = threadIdx.x;
     const int id = i < n ? ids[i] : -1;
@@ -127,6 +128,7 @@ __global__ void __launch_bounds__(kT)
 __global__ void __launch_bounds__(kT)
     fork_kernel(const __grid_constant__ PagedParams p, const int *src, const int *dst, int n,
                 int *status) {
+    wait_previous_kernel();
     __shared__ int s_dst[kT], s_free[kT];
     const PagedScratch x = paged_scratch(p.scratch, p.P);
     const int i = threadIdx.x;
@@ -282,6 +284,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 // One warp per (entry, stretch of 32 pages): the page's last holder marks it.
 __global__ void __launch_bounds__(256)
     release_kernel(const __grid_constant__ PagedParams p, const int *ids, int n, int *status) {
+    wait_previous_kernel();
     const PagedScratch x = paged_scratch(p.scratch, p.P);
     const int lane = threadIdx.x & 31;
     const int warps = gridDim.x * 8, w0 = blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -348,6 +351,7 @@ __global__ void __launch_bounds__(kT)
 
 // ------------------------------------------------------------------ compact
 __global__ void __launch_bounds__(kT) compact_kernel(const __grid_constant__ PagedParams p) {
+    wait_previous_kernel();
     const PagedScratch x = paged_scratch(p.scratch, p.P);
     const int i = threadIdx.x;
     int used = 0;
@@ -415,6 +419,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 __global__ void __launch_bounds__(kT)
     copy_list_kernel(const __grid_constant__ PagedParams p, const int *src, const int *dst, int n,
                      int *status) {
+    wait_previous_kernel();
     __shared__ int s_src[kT], s_dst[kT];
     const PagedScratch x = paged_scratch(p.scratch, p.P);
     const int i = threadIdx.x;
@@ -568,9 +573,10 @@ extern "C" lcx_status lcx_pages_extend(const lcx_paged_cache *cache, const int32
     lcx_status st = paged_prepare(cache, p);
     if (st != LCX_OK) return st;
     if ((st = entries_ok(seq_ids, start, n, "extend")) != LCX_OK || n == 0) return st;
-    extend_kernel<<<1, deciding(n), 0, static_cast<cudaStream_t>(stream)>>>(p, seq_ids, n_new, int(n),
-                                                                   start, dev_status);
-    return launched(cudaSuccess, "pages_extend");
+    return launched(launch_dependent(extend_kernel, dim3(1), dim3(deciding(n)), 0,
+                                     static_cast<cudaStream_t>(stream), p, seq_ids, n_new, int(n),
+                                     start, dev_status),
+                    "pages_extend");
 }
 
 extern "C" lcx_status lcx_pages_fork(const lcx_paged_cache *cache, const int32_t *src,
@@ -582,8 +588,10 @@ extern "C" lcx_status lcx_pages_fork(const lcx_paged_cache *cache, const int32_t
     if (st != LCX_OK) return st;
     if ((st = entries_ok(src, dst, n, "fork")) != LCX_OK || n == 0) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    fork_kernel<<<1, deciding(n), 0, s>>>(p, src, dst, int(n), dev_status);
-    if ((st = launched(cudaSuccess, "pages_fork")) != LCX_OK) return st;
+    if ((st = launched(launch_dependent(fork_kernel, dim3(1), dim3(deciding(n)), 0, s, p, src, dst,
+                                        int(n), dev_status),
+                       "pages_fork")) != LCX_OK)
+        return st;
     return launched(launch_dependent(fork_apply_kernel, dim3(device_sms() * kCopyCtas),
                                      dim3(kCopyThreads), 0, s, p, page_shape(p), src, dst, int(n),
                                      dev_status),
@@ -600,8 +608,10 @@ extern "C" lcx_status lcx_pages_free(const lcx_paged_cache *cache, const int32_t
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const long long warps = n * ((p.MP + 31) / 32);
     const unsigned grid = unsigned(std::min<long long>((warps + 7) / 8, device_sms() * kCopyCtas));
-    release_kernel<<<grid, 256, 0, s>>>(p, seq_ids, int(n), dev_status);
-    if ((st = launched(cudaSuccess, "pages_free")) != LCX_OK) return st;
+    if ((st = launched(launch_dependent(release_kernel, dim3(grid), dim3(256), 0, s, p, seq_ids,
+                                        int(n), dev_status),
+                       "pages_free")) != LCX_OK)
+        return st;
     return launched(launch_dependent(collect_kernel, dim3(1), dim3(kT), 0, s, p, seq_ids, int(n),
                                      dev_status),
                     "pages_free");
@@ -614,8 +624,9 @@ extern "C" lcx_status lcx_pages_compact(const lcx_paged_cache *cache, int32_t *d
     lcx_status st = paged_prepare(cache, p);
     if (st != LCX_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    compact_kernel<<<1, kT, 0, s>>>(p);
-    if ((st = launched(cudaSuccess, "pages_compact")) != LCX_OK) return st;
+    if ((st = launched(launch_dependent(compact_kernel, dim3(1), dim3(kT), 0, s, p),
+                       "pages_compact")) != LCX_OK)
+        return st;
     return launched(launch_dependent(compact_apply_kernel, dim3(device_sms() * kCopyCtas),
                                      dim3(kCopyThreads), 0, s, p, page_shape(p), dev_status),
                     "pages_compact");
@@ -630,8 +641,10 @@ extern "C" lcx_status lcx_pages_copy(const lcx_paged_cache *cache, const int32_t
     if (st != LCX_OK) return st;
     if ((st = entries_ok(src_pages, dst_pages, n, "copy")) != LCX_OK || n == 0) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    copy_list_kernel<<<1, deciding(n), 0, s>>>(p, src_pages, dst_pages, int(n), dev_status);
-    if ((st = launched(cudaSuccess, "pages_copy")) != LCX_OK) return st;
+    if ((st = launched(launch_dependent(copy_list_kernel, dim3(1), dim3(deciding(n)), 0, s, p,
+                                        src_pages, dst_pages, int(n), dev_status),
+                       "pages_copy")) != LCX_OK)
+        return st;
     return launched(launch_dependent(copy_kernel, dim3(device_sms() * kCopyCtas), dim3(kCopyThreads), 0, s,
                                      p, page_shape(p)),
                     "pages_copy");

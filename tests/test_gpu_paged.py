@@ -476,3 +476,70 @@ def test_a_cache_keeps_its_buffers():
                     if name != "page_size" else 32)
     cache.seq_lens += 0          # in place
     cache.reset()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_behind_copies_and_fills(captured):
+    """Every call's first kernel is a programmatic dependent of what lies before it in the
+    stream: copies from the host, fills and small kernels are seen, in a stream and in
+    a captured graph."""
+    rope = lcx.RopeParams("plain", 64)
+    n, L = 8, 600
+    cache = lcx.PagedCache(n * 40, 16, 2, 64, n, 40)
+    dev = torch.device("cuda")
+    ids = torch.zeros(n, dtype=torch.int32, device=dev)
+    host_ids = torch.arange(n, dtype=torch.int32).pin_memory()
+    cu = torch.arange(0, n * L + 1, L, dtype=torch.int32, device=dev)
+    new = torch.full((n,), L, dtype=torch.int32, device=dev)
+    start = torch.empty_like(ids)
+    g = torch.Generator().manual_seed(5)
+    hk, hv, hq = (torch.randn((m, h, 64), generator=g).bfloat16().pin_memory()
+                  for m, h in ((n * L, 2), (n * L, 2), (n, 4)))
+    k, v, q, o = (torch.zeros(t.shape, dtype=torch.bfloat16, device=dev) for t in (hk, hv, hq, hq))
+    qp = torch.zeros((n * L, 4, 64), dtype=torch.bfloat16, device=dev)
+    op = torch.empty_like(qp)
+    plan = lcx.VarlenPlan([L] * n)
+    ws = torch.empty(lcx.paged_decode_workspace_bytes(cache, n, 4), dtype=torch.uint8, device=dev)
+    wp = torch.empty(lcx.varlen_workspace_bytes(plan, 2, 64, k.dtype), dtype=torch.uint8, device=dev)
+    status = torch.ones(1, dtype=torch.int32, device=dev)
+
+    def step():
+        status.zero_()
+        ids.copy_(host_ids, non_blocking=True)
+        lcx.pages_extend(cache, ids, new, start=start, status=status)
+        k.copy_(hk, non_blocking=True)
+        v.copy_(hv, non_blocking=True)
+        lcx.paged_append(cache, k, v, ids, start, rope, cu_new=cu, status=status)
+        q.copy_(hq, non_blocking=True)
+        lcx.paged_decode(cache, q, ids, rope, out=o, workspace=ws, status=status)
+        qp[L - 1::L].copy_(q)
+        lcx.attn_varlen(qp, k, v, plan, rope, out=op, workspace=wp, status=status)
+        k.zero_()
+        v.zero_()
+        lcx.pages_free(cache, ids, status=status)
+        ids.zero_()
+        q.zero_()
+
+    if captured:
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            step()
+        torch.cuda.current_stream().wait_stream(s)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+    for _ in range(3):
+        o.zero_()
+        op.zero_()
+        graph.replay() if captured else step()
+        assert int(status) == 0 and int(cache.n_free) == n * 40
+        pos = torch.arange(L)
+        for i in range(n):
+            kk, vv = hk[i * L:(i + 1) * L], hv[i * L:(i + 1) * L]
+            # the cache holds the rotated keys rounded to bf16; the library's max-abs tolerance
+            kr = rotate(kk, pos, rope).bfloat16().double()
+            qr = rotate(hq[i:i + 1], pos[-1:], rope)
+            want = attend(qr, kr, vv.double(), pos[-1:], True, 0, 0, 0.125)[0]
+            assert (o[i].double().cpu() - want[0]).abs().max() <= 2e-2
+            assert (op[(i + 1) * L - 1].double().cpu() - want[0]).abs().max() <= 2e-2
