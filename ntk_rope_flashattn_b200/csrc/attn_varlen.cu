@@ -12,7 +12,7 @@
 // tile of scores goes through both in turn.  Measured: 4.2k cycles per key tile (2048
 // of tensor-core work) and 14-16k per CTA outside of the key loop, the query's copy,
 // rotation and the output.  16384 tokens of 32 heads: 1030 TFLOP/s (2.1 ms); 12
-// prompts of 200 to 4100: 600 TFLOP/s (386 us); 8 x 2048: 671.  (Persistent CTAs whose
+// prompts of 200 to 4100: 600 TFLOP/s (384 us); 8 x 2048: 670.  (Persistent CTAs whose
 // helpers rotate the next block's queries meanwhile: 560-612 us where this takes 410.
 // The rotation's warps take issue slots from the softmax: 4.7-5.8k cycles per tile.)
 // One CTA per (row block of the plan, pair of query heads), 16 warps:

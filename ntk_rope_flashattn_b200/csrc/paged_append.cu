@@ -13,8 +13,8 @@
 // 16-byte vector of pairs of a token, evaluates their cos/sin once and walks
 // the slice.  The token's sequence, position and page are found once per token
 // by one thread.
-// Measured: 12 prompts (14k tokens, 32 query and 8 kv heads of 128, bf16), 0.46 GB: 79 us,
-// 5.9 TB/s of a copy's 6.5; 64 single tokens: 6.2 us, two launches' latency.
+// Measured: 12 prompts (14k tokens, 32 query and 8 kv heads of 128, bf16), 0.46 GB: 81 us,
+// 5.7 TB/s of a copy's 6.5; 64 single tokens: 5.6 us, a launch and a chain of loads.
 #include <algorithm>
 
 #include "paged.cuh"

@@ -9,8 +9,8 @@
 // Bound by HBM: every visible key and value is read once, 4 Hkv D bytes per key
 // (bf16) against 4 Hq D flops.  Measured (8 kv heads of 128, bf16): 1.39 GB of keys and
 // values in 208 us, 6.7 TB/s, as fast as a copy; 0.35 GB in 64.5 us, 5.4 TB/s (the start,
-// the uneven end and the join are 11 us); 4 short sequences in 7.6 us.  fp32: 0.40 GB
-// in 89 us, 4.5 TB/s.
+// the uneven end and the join are 11 us); one sequence of 300 keys in 7.1 us.  fp32:
+// 0.40 GB in 86 us, 4.7 TB/s, bound by the arithmetic of the parts.
 //
 // Work: the visible keys of each (entry, kv head, block of query heads), a
 // "segment", are cut into blocks of 32 to 128 keys; the blocks of all segments in
