@@ -20,7 +20,7 @@ import ctypes
 import functools
 import struct
 
-from . import RopeParams, _check, _dtype_code, _RopeParams, _same_device, load
+from . import RopeParams, _check, _dtype_code, _RopeParams, load
 
 LCX_ERR_NO_PAGES = 5
 LCX_PAGES_MAX_ENTRIES = 1024
@@ -105,7 +105,7 @@ def _declare(lib):
 _FIXED = frozenset(("k_pages", "v_pages", "meta", "block_table", "seq_lens", "ref_counts",
                     "free_pages", "n_free", "scratch", "num_pages", "page_size", "kv_heads",
                     "head_dim", "max_seqs", "max_pages_per_seq", "num_layers", "dtype", "device",
-                    "_struct"))
+                    "_struct", "_dev"))
 
 
 class PagedCache:
@@ -135,7 +135,7 @@ class PagedCache:
                 raise ValueError("%s must be positive (got %s)" % (name, x))
             setattr(self, name, int(x))
         shape = (self.num_layers, self.num_pages, self.page_size, self.kv_heads, self.head_dim)
-        self.device, self.dtype = device, dtype
+        self.device, self.dtype, self._dev = device, dtype, device.index
         pools = []
         for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
             if t is None:
@@ -195,14 +195,14 @@ class PagedCache:
 def _index(cache, **tensors):
     """Index arguments: contiguous int32 vectors on the cache's device."""
     import torch
-    out = []
+    out, dev, int32 = [], cache._dev, torch.int32
     for name, t in tensors.items():
         if t is None:
             out.append(0)
             continue
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1:
+        if not isinstance(t, torch.Tensor) or t.dtype is not int32 or t.dim() != 1:
             raise ValueError("%s must be a 1-D int32 tensor" % name)
-        if t.device != cache.device:
+        if t.get_device() != dev:
             raise ValueError("%s must be a CUDA tensor on %s (got %s)" % (name, cache.device,
                                                                          t.device))
         if not t.is_contiguous():
@@ -211,18 +211,33 @@ def _index(cache, **tensors):
     return out
 
 
+def _on_device(dev, **tensors):
+    """Every tensor given (None skipped) must lie on CUDA device `dev`."""
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError("%s must be a CUDA tensor on cuda:%d (got %s)" % (name, dev, t.device))
+
+
+def _current_stream(dev):
+    """The handle of device `dev`'s current stream (without a Stream object, where torch
+    gives it so: 0.2 instead of 1.3 us)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if raw else torch.cuda.current_stream(dev).cuda_stream
+
+
 def _call_on(dev, call, *args):
     """call(*args, stream) with device `dev` current, on its current stream."""
     import torch
     if torch.cuda.current_device() == dev:
-        _check(call(*args, torch.cuda.current_stream(dev).cuda_stream))
+        _check(call(*args, _current_stream(dev)))
     else:
         with torch.cuda.device(dev):
-            _check(call(*args, torch.cuda.current_stream(dev).cuda_stream))
+            _check(call(*args, _current_stream(dev)))
 
 
 def _launch(cache, call, *args):
-    _call_on(cache.device.index, call, *args)
+    _call_on(cache._dev, call, *args)
 
 
 def pages_extend(cache, seq_ids, n_new=None, start=None, status=None):
@@ -271,7 +286,8 @@ def pages_copy(cache, src_pages, dst_pages, status=None):
 
 
 def _tokens(t, name, heads, D, dtype):
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != D:
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or shape[2] != D:
         raise ValueError("%s must be [tokens, %s, %d], got %s" % (name, heads or "heads", D,
                                                                   tuple(t.shape)))
     if t.dtype != dtype:
@@ -304,9 +320,7 @@ def paged_append(cache, k, v, seq_ids, start, rope: RopeParams, layer: int = 0, 
     given; q itself rotates in place).  k_out receives the rotated keys packed
     like k.  Returns q_out (None without q)."""
     import torch
-    if not k.is_cuda:
-        raise ValueError("k must be a CUDA tensor on %s (got %s)" % (cache.device, k.device))
-    _same_device(cache.k_pages, k=k, v=v, q=q, q_out=q_out, k_out=k_out)
+    _on_device(cache._dev, k=k, v=v, q=q, q_out=q_out, k_out=k_out)
     H, D = cache.kv_heads, cache.head_dim
     _tokens(k, "k", H, D, cache.dtype)
     _tokens(v, "v", H, D, cache.dtype)
@@ -374,9 +388,7 @@ def paged_decode(cache, q, seq_ids, rope: RopeParams, layer: int = 0, window: in
     tensor, 256-byte aligned) is allocated when not given; calls in flight at the
     same time, replayed graphs among them, must not share one."""
     import torch
-    if not q.is_cuda:
-        raise ValueError("q must be a CUDA tensor on %s (got %s)" % (cache.device, q.device))
-    _same_device(cache.k_pages, q=q, out=out, lse=lse, workspace=workspace)
+    _on_device(cache._dev, q=q, out=out, lse=lse, workspace=workspace)
     _tokens(q, "q", None, cache.head_dim, cache.dtype)
     n, Hq = q.shape[0], q.shape[1]
     if seq_ids.shape != (n,):

@@ -8,8 +8,8 @@ import ctypes
 
 import numpy as np
 
-from . import RopeParams, _check, _dtype_code, _RopeParams, _same_device, load
-from .paged import _call_on, _packer, _raw, _rope_c
+from . import RopeParams, _check, _dtype_code, _RopeParams, load
+from .paged import _call_on, _on_device, _packer, _raw, _rope_c
 
 LCX_VARLEN_PREROTATED = 1
 LCX_VARLEN_TEST_STALL = 0x80000000
@@ -125,7 +125,8 @@ def attn_varlen(q, k, v, plan: VarlenPlan, rope: RopeParams, causal: bool = True
     share one).  A query without a visible key gets
     o = 0 and lse = -inf.  ``status`` and ``watchdog_ms`` as for ``attn_fwd``."""
     import torch
-    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or not (q.is_cuda and k.is_cuda and v.is_cuda):
+    dev = q.get_device()
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or dev < 0:
         raise ValueError("q, k, v must be 3-D CUDA tensors [tokens, heads, D]")
     Tq, Hq, D = q.shape
     Tk, Hkv, Dk = k.shape
@@ -133,8 +134,8 @@ def attn_varlen(q, k, v, plan: VarlenPlan, rope: RopeParams, causal: bool = True
         raise ValueError("shape mismatch: q %s k %s v %s" % (q.shape, k.shape, v.shape))
     if not (q.dtype == k.dtype == v.dtype):
         raise ValueError("q, k, v must share a dtype")
-    _same_device(q, k=k, v=v, out=out, lse=lse, workspace=workspace, status=status,
-                 plan=plan.plan)
+    _on_device(dev, k=k, v=v, out=out, lse=lse, workspace=workspace, status=status,
+               plan=plan.plan)
     alloc = q.new_empty if plan.total_q == Tq else q.new_zeros
     o = out if out is not None else alloc((Tq, Hq, D))
     if o.shape != q.shape or o.dtype != q.dtype:
@@ -159,5 +160,5 @@ def attn_varlen(q, k, v, plan: VarlenPlan, rope: RopeParams, causal: bool = True
         *o.stride(), rope_c, int(window), int(sinks), float(softmax_scale),
         (LCX_VARLEN_PREROTATED if prerotated else 0) |
         (LCX_VARLEN_TEST_STALL if _test_stall else 0), int(watchdog_ms), 0)
-    _call_on(q.device.index, _raw("lcx_attn_varlen", 1), a)
+    _call_on(dev, _raw("lcx_attn_varlen", 1), a)
     return (o, lse) if return_lse else o
