@@ -318,7 +318,8 @@ def paged_append(cache, k, v, seq_ids, start, rope: RopeParams, layer: int = 0, 
     cu_new) at positions from start[i] on (``pages_extend`` gives it).  With q
     [T, Hq, D] the queries are rotated along, into q_out (allocated when not
     given; q itself rotates in place).  k_out receives the rotated keys packed
-    like k.  Returns q_out (None without q)."""
+    like k.  Rows of skipped entries are not written: those of a q_out that the call
+    allocates hold nothing.  Returns q_out (None without q)."""
     import torch
     _on_device(cache._dev, k=k, v=v, q=q, q_out=q_out, k_out=k_out)
     H, D = cache.kv_heads, cache.head_dim

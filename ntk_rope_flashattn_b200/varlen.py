@@ -123,7 +123,7 @@ def attn_varlen(q, k, v, plan: VarlenPlan, rope: RopeParams, causal: bool = True
     ``workspace`` (uint8, 256-byte aligned, ``varlen_workspace_bytes``; allocated when
     not given; calls in flight at the same time, replayed graphs among them, must not
     share one).  A query without a visible key gets
-    o = 0 and lse = -inf.  ``status`` and ``watchdog_ms`` as for ``attn_fwd``."""
+    o = 0 and lse = -inf.  ``out`` does not overlap k or v.  ``status`` and ``watchdog_ms`` as for ``attn_fwd``."""
     import torch
     dev = q.get_device()
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or dev < 0:
