@@ -308,6 +308,29 @@ def test_replays_from_a_graph_and_other_streams():
         assert torch.equal(out, lcx.attn_varlen(q, k, v, plan, rope))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_calls_at_once_on_two_streams(dt):
+    """One plan, one set of keys, two streams, a workspace for each call in flight."""
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    rope = lcx.RopeParams("plain", 64)
+    plan = lcx.VarlenPlan([300, 7, 450])
+    k, v = (randn(i, 757, 2, 64, dtype=dtype) for i in (2, 3))
+    qs = [randn(10 + i, 757, 4, 64, dtype=dtype) for i in range(2)]
+    want = [lcx.attn_varlen(q, k, v, plan, rope) for q in qs]
+    need = lcx.varlen_workspace_bytes(plan, 2, 64, dtype)
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in qs]
+    outs = [[torch.empty_like(q) for _ in range(8)] for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    for r in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                lcx.attn_varlen(qs[i], k, v, plan, rope, workspace=ws[i], out=outs[i][r])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in outs[i])
+
+
 def test_a_plan_that_is_not_the_tensors_is_refused():
     rope = lcx.RopeParams("plain", 64)
     q, k = randn(0, 10, 2, 64), randn(1, 10, 2, 64)
