@@ -659,7 +659,7 @@ struct Bars {
     // per pair (pair e of job q at e CPR + q: a warp's lanes read neighbours), for the
     // query rotation (lanes read different entries, which the
     // parameter space would serve one after the other): the angle of the block's first
-    // position reduced to [-pi, pi], theta in two fp32 parts, cos and sin of the step
+    // position and theta (in two fp32 parts) reduced to [-pi, pi], cos and sin of the step
     float base[D / 2];
     float2 theta[D / 2], step[D / 2];
 };
@@ -749,9 +749,10 @@ __device__ __forceinline__ void rotate_queries(const Block &b, int tid, uint8_t 
     float2 st[J::PPJ];
 #pragma unroll
     for (int e = 0; e < J::PPJ; ++e) {
-        // The row's angle r0 theta (r0 < 96) on top of the block's: 2 pi in two parts, the
-        // first of 16 bits so that its multiples are exact; within 2^-22 in all.  (The
-        // fp64 reduction per thread took 2.3k cycles of the 384 threads.)
+        // The row's angle r0 theta on top of the block's, r0 < 96 and |theta| <= pi (its
+        // whole turns left out): below 48 turns.  2 pi in two parts, the first of 17 bits
+        // so that these multiples are exact; within 2^-22 in all.  (The fp64 reduction per
+        // thread took 2.3k cycles of the 384 threads.)
         const float2 th = bar.theta[e * J::CPR + q];
         const float r = static_cast<float>(r0);
         const float k = rintf(r * th.x * 0.15915494f);
@@ -953,9 +954,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int i = threadIdx.x - 128;
         using J = Job<D, kHalf>;
         const int at = i % J::PPJ * J::CPR + i / J::PPJ;
-        const double th = v.theta[i];
+        // (rows are whole numbers: whole turns of theta leave their angles as they are)
+        const double th = rope_reduced(v.theta[i]);
         const float hi = static_cast<float>(th);
-        bar.base[at] = rope_reduced_angle((long long)b0.u.pos0, th);
+        bar.base[at] = rope_reduced_angle((long long)b0.u.pos0, v.theta[i]);
         bar.theta[at] = make_float2(hi, static_cast<float>(th - hi));
         bar.step[at] = p.step[i];
     }

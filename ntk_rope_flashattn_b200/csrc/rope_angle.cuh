@@ -14,24 +14,22 @@ constexpr double kTwoPiHi = 6.283185307179586;
 constexpr double kTwoPiLo = 2.4492935982947064e-16;
 constexpr double kInvTwoPi = 0.15915494309189535;
 
+// phi - 2 pi k in [-pi, pi], in fp64.
+__device__ __forceinline__ double rope_reduced(double phi) {
+    const double k = rint(phi * kInvTwoPi);
+    return fma(-k, kTwoPiLo, fma(-k, kTwoPiHi, phi));
+}
+
 // m * theta reduced to [-pi, pi] (fp32).
 __device__ __forceinline__ float rope_reduced_angle(long long m, float theta) {
-    const double phi = static_cast<double>(m) * static_cast<double>(theta);
-    const double k = rint(phi * kInvTwoPi);
-    double r = fma(-k, kTwoPiHi, phi);
-    r = fma(-k, kTwoPiLo, r);
-    return static_cast<float>(r);
+    return static_cast<float>(rope_reduced(static_cast<double>(m) * static_cast<double>(theta)));
 }
 
 // The same for a frequency in fp64: the product is rounded once (2^-53 of the
-// angle), so positions up to 2^30 keep the angle to 2^-23 rad before the rounding
+// angle), so with theta <= 1 positions up to 2^30 keep it to 2^-23 rad before the rounding
 // to fp32.
 __device__ __forceinline__ float rope_reduced_angle(long long m, double theta) {
-    const double phi = static_cast<double>(m) * theta;
-    const double k = rint(phi * kInvTwoPi);
-    double r = fma(-k, kTwoPiHi, phi);
-    r = fma(-k, kTwoPiLo, r);
-    return static_cast<float>(r);
+    return static_cast<float>(rope_reduced(static_cast<double>(m) * theta));
 }
 
 // Accurate (libm) cosine and sine of m * theta.

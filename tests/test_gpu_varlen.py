@@ -395,3 +395,27 @@ def test_lse_of_short_rows_is_precise():
     o, lse = lcx.attn_varlen(q, k, v, plan, rope, window=9, sinks=1, return_lse=True)
     w = plain(q, k, v, lens, lens, rope, True, 9, 1)
     assert (lse.double().cpu() - w[1]).abs().max() <= 3e-5
+
+
+# Pair frequencies above 1 (context shrunk: scale or factors below 1): angles many turns
+# a token, which keys and queries must reduce alike.
+FAST = [("pi", dict(scale=0.01)), ("factors", 1e-3), ("factors", 1e-6)]
+
+
+@pytest.mark.parametrize("pairing", ["half", "interleaved"])
+@pytest.mark.parametrize("lens,Hq,H,D", [([60, 127, 300], 4, 2, 128), ([60, 127, 300], 3, 1, 64),
+                                         ([300] * 10, 32, 2, 64), ([300] * 10, 30, 2, 128)])
+@pytest.mark.parametrize("mode,kw", FAST)
+def test_frequencies_above_one(mode, kw, lens, Hq, H, D, pairing):
+    """Angles of up to 10^8 rad: within the bounds of any other, and lse of short rows
+    within 3e-5 (the angles add 2^-22 rad a pair to the bound derived below)."""
+    if mode == "factors":
+        kw = dict(factors=[kw] * (D // 2))
+    rope = lcx.RopeParams(mode, D, original_max_pos=64, pairing=pairing, **kw)
+    n = sum(lens)
+    q, k, v = (randn(i, n, h, D) for i, h in ((1, Hq), (2, H), (3, H)))
+    o, lse = lcx.attn_varlen(q, k, v, lcx.VarlenPlan(lens), rope, return_lse=True)
+    want = plain(q, k, v, lens, lens, rope)
+    compare(o, lse, want, torch.bfloat16, max(lens), mode)
+    short = torch.cat([torch.arange(x) < 127 for x in lens])
+    assert ((lse.double().cpu() - want[1]).abs()[:, short]).max() <= 3e-5
