@@ -391,7 +391,9 @@ LCX_API lcx_status lcx_attn_fwd_split_static(const lcx_attn_args *args, int32_t 
  * never writes into a shared page.  Device-side checks: a page number outside
  * [0, num_pages) is never followed (its keys count as hidden), and such an
  * entry, a bad sequence number or a lack of pages is reported through the
- * optional dev_status word (written, never cleared) with the entry skipped.
+ * optional dev_status word (written, never cleared) with the entry skipped.  One
+ * word may serve several calls: a code stays unless a larger one follows, and
+ * LCX_ERR_TIMEOUT (an attention call's results are undefined) outranks all.
  * Angles: this section and the next form m * theta'_i from the fp64 frequencies,
  * lcx_apply_rope and lcx_attn_fwd from lcx_rope_table's fp32 values; at position
  * m the two differ by at most m theta'_i 2^-24 rad.

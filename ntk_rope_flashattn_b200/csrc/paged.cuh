@@ -37,9 +37,21 @@ inline long long paged_scratch_ints(long long P) {
     return 4 + 4ll * LCX_PAGES_MAX_ENTRIES + 4 * P;
 }
 
-// The first non-zero status stays unless a larger code follows.
+// A status stays unless a larger code follows; LCX_ERR_TIMEOUT (results undefined)
+// replaces every other one and stays.  (`code` is a constant: one branch is left.)
 __device__ __forceinline__ void raise_status(int *status, int code) {
-    if (status) atomicMax(status, code);
+    if (!status) return;
+    if (code == LCX_ERR_TIMEOUT) {
+        atomicExch(status, code);
+    } else if (code < LCX_ERR_TIMEOUT) {
+        atomicMax(status, code);
+    } else {
+        for (int was = 0;;) {               // (every other writer raises it: a few turns)
+            const int now = atomicCAS(status, was, code);
+            if (now == was || now >= code || now == LCX_ERR_TIMEOUT) break;
+            was = now;
+        }
+    }
 }
 
 // Validate `c` and fill `x`.
