@@ -182,7 +182,8 @@ typedef struct {
                                   After an expiry o and lse are undefined (the call
                                   still returns LCX_OK: the expiry happens on the
                                   device after the call returned), so callers that
-                                  must detect it pass this word and read it      */
+                                  must detect it pass this word and read it.  Codes
+                                  that other calls left in it play no part       */
     int32_t dtype;             /* lcx_dtype of q, k, v, o                         */
     int32_t causal;            /* 1 = key j visible to query i only if j <= i    */
     int64_t B, Hq, Hkv, L, D;  /* Hq % Hkv == 0; D = query/key head dim           */

@@ -912,8 +912,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A CTA that starts after another one's watchdog fired gives up at its
     // first wait that does not complete at once: thread 0 reads the status
     // word here, after the barrier, so no role waits for that load to start.
-    bool pre = false;   // thread 0: the word was already set
-    if (threadIdx.x == 0 && p.status && *reinterpret_cast<volatile int *>(p.status) != 0) {
+    bool pre = false;   // thread 0: the word held the timeout already
+    if (threadIdx.x == 0 && p.status &&
+        *reinterpret_cast<volatile int *>(p.status) == int(LCX_ERR_TIMEOUT)) {
         pre = true;
         *abort = 1;
     }
@@ -2008,8 +2009,9 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
     // A CTA that starts after another one's watchdog fired gives up at its
     // first wait that does not complete at once (the status word is read by
     // thread 0 after the barrier, off the roles' path).
-    bool pre = false;   // thread 0: the word was already set
-    if (threadIdx.x == 0 && p.status && *reinterpret_cast<volatile int *>(p.status) != 0) {
+    bool pre = false;   // thread 0: the word held the timeout already
+    if (threadIdx.x == 0 && p.status &&
+        *reinterpret_cast<volatile int *>(p.status) == int(LCX_ERR_TIMEOUT)) {
         pre = true;
         *abort = 1;
     }

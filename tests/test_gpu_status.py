@@ -36,3 +36,20 @@ def test_a_timeout_outlasts_other_reports(first):
     for c in calls if first == "pages" else calls[::-1]:
         c()
     assert int(status) == lcx.LCX_ERR_TIMEOUT
+
+
+@pytest.mark.parametrize("code", ["LCX_ERR_INVALID_ARG", "LCX_ERR_NO_PAGES"])
+@pytest.mark.parametrize("L,Lq,splits", [(700, 700, 0), (700, 1, 0), (700, 1, 4)])
+def test_attn_fwd_runs_with_another_calls_report(code, L, Lq, splits):
+    """attn_fwd gives up early on a timeout only: a page call's report in the word leaves
+    its results, and the word, alone."""
+    rope = lcx.RopeParams("plain", 128)
+    q, k, v = randn(1, 1, 8, Lq, 128), randn(2, 1, 2, L, 128), randn(3, 1, 2, L, 128)
+    kw = dict(num_splits=splits) if splits else {}
+    want, wl = lcx.attn_fwd(q, k, v, rope, q_offset=L - Lq, return_lse=True, **kw)
+    status = ints([getattr(lcx, code)])
+    out = torch.full_like(want, 7.0)
+    o, lse = lcx.attn_fwd(q, k, v, rope, q_offset=L - Lq, return_lse=True, status=status, out=out,
+                          **kw)
+    assert torch.equal(o, want) and torch.equal(lse, wl)
+    assert int(status) == getattr(lcx, code)
