@@ -619,7 +619,9 @@ typedef struct {
  *   rotated inputs enter as they are; the weights rounded to bf16, their sum not.
  *   fp32: every operand of a product as two tf32 parts (within 2^-21 of it).
  *   dev_status: LCX_ERR_TIMEOUT after an expired wait, as lcx_attn_fwd (o and lse
- *   are then undefined); LCX_ERR_INVALID_ARG for a plan that is not info's.
+ *   are then undefined); LCX_ERR_INVALID_ARG for a device plan with row blocks outside
+ *   the tensors, whose rows stay as they were (no other difference from the plan that
+ *   info belongs to is noticed).
  */
 LCX_API lcx_status lcx_attn_varlen(const lcx_varlen_args *args, void *stream);
 

@@ -107,6 +107,8 @@ __global__ void __launch_bounds__(kF32Threads, F32<D>::kCtas)
     const VarlenUnit U = load_unit(p, uu >> 1);
     const int r0 = (uu & 1) * kRows, rows = min(kRows, U.rows - r0);
     if (rows <= 0) {
+        // (a plan that does not fit the tensors, or a block of up to kRows rows: no second half)
+        if (U.rows <= 0 && threadIdx.x == 0) raise_status(p.status, LCX_ERR_INVALID_ARG);
         wait_previous_kernel();      // what follows in the stream may write k
         return;
     }

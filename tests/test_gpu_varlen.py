@@ -419,3 +419,22 @@ def test_frequencies_above_one(mode, kw, lens, Hq, H, D, pairing):
     compare(o, lse, want, torch.bfloat16, max(lens), mode)
     short = torch.cat([torch.arange(x) < 127 for x in lens])
     assert ((lse.double().cpu() - want[1]).abs()[:, short]).max() <= 3e-5
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_rows_of_a_foreign_plan_are_left_out_and_reported(dt):
+    """A device plan whose second sequence ends behind the tensors: its rows stay as they
+    were, the status word says so, the first sequence's are right."""
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    rope = lcx.RopeParams("plain", 64)
+    lens = [100, 101]
+    plan, other = lcx.VarlenPlan(lens), lcx.VarlenPlan([100, 128])
+    plan.plan.copy_(other.plan)
+    q, k, v = (randn(i, 201, h, 64, dtype=dtype) for i, h in ((1, 4), (2, 2), (3, 2)))
+    out, lse = torch.full_like(q, 5.0), torch.full((4, 201), 5.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lcx.attn_varlen(q, k, v, plan, rope, out=out, lse=lse, status=status)
+    assert int(status) == lcx.LCX_ERR_INVALID_ARG
+    assert (out[100:] == 5).all() and (lse[:, 100:] == 5).all()
+    compare(out[:100], lse[:, :100], plain(q[:100], k[:100], v[:100], [100], [100], rope), dtype,
+            100)
