@@ -610,7 +610,9 @@ typedef struct {
  * lcx_attn_fwd.  A query without a visible key (no keys, or more queries than
  * keys) gets o = 0, lse = -inf.  Rows of o and lse at total_q and beyond are
  * left as they were.  NaN or infinity in a key or value that a query does not
- * see leaves that query alone.
+ * see leaves that query alone.  An infinite key that it sees: a logit of -inf has the
+ * weight 0, any other makes the row NaN (bf16 keys that the call rotates: the row may
+ * be NaN either way).
  *   Supported: D 64 or 128, full rotary; o does not overlap k or v; bf16: no
  *   stride of 0.
  *   Arithmetic: bf16: tensor-core products with fp32 accumulation; q' and k'

@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kF32Threads, F32<D>::kCtas)
                 for (int e = 0; e < 2; ++e) {
                     float &x = s[n][2 * r + e];
                     x = whole || sees(key0 + 8 * n + e, pos + 8 * r)
-                            ? (x + low[n][2 * r + e]) * p.c_log2
+                            ? join(x, low[n][2 * r + e]) * p.c_log2
                             : -INFINITY;
                     mx[r] = fmaxf(mx[r], x);
                 }

@@ -26,10 +26,17 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
 
 // x in two tf32 parts, both cut, not rounded (two cheap instructions; the matrix
 // instruction reads a value's first 19 bits): x - hi is exact and lo counts with its
-// first 11 bits, so hi + lo is within 2^-21 of x.  A NaN or infinite x has a NaN part.
+// first 11 bits, so hi + lo is within 2^-21 of x.  A NaN or infinite x has a NaN lo, and
+// itself as hi (but for a NaN with nothing but low payload bits, which no arithmetic makes).
 __device__ __forceinline__ void tf32_parts(float x, uint32_t &hi, uint32_t &lo) {
     hi = __float_as_uint(x) & 0xffffe000u;
     lo = __float_as_uint(x - __uint_as_float(hi));
+}
+
+// hi + lo, sums of products with the parts, where lo is a correction: an infinite or NaN
+// hi stands alone.
+__device__ __forceinline__ float join(float hi, float lo) {
+    return fabsf(hi) < INFINITY ? hi + lo : hi;
 }
 
 // Four 8 x 8 blocks of 16-bit values; lane l gives the address of row l % 8 of

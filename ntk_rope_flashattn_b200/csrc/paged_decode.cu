@@ -194,10 +194,6 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint3
     hi = pk(x, y);
     lo = pk(x - bf16lo_to_f32(hi), y - bf16hi_to_f32(hi));
 }
-// hi + lo where lo is a correction: an infinite or NaN hi stands alone.
-__device__ __forceinline__ float join(float hi, float lo) {
-    return fabsf(hi) < INFINITY ? hi + lo : hi;
-}
 
 // ------------------------------------------------------------------ kernel
 template <typename T, int D, bool kWide>

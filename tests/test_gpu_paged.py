@@ -543,3 +543,21 @@ def test_calls_behind_copies_and_fills(captured):
             want = attend(qr, kr, vv.double(), pos[-1:], True, 0, 0, 0.125)[0]
             assert (o[i].double().cpu() - want[0]).abs().max() <= 2e-2
             assert (op[(i + 1) * L - 1].double().cpu() - want[0]).abs().max() <= 2e-2
+
+
+@pytest.mark.parametrize("Hq", [4, 24])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_decode_key_at_minus_infinity_weighs_nothing(dt, Hq):
+    """A logit of -inf (an infinite cached key) has the weight 0, as in attn_varlen."""
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    rope = lcx.RopeParams("plain", 64)
+    c, rows = cache_of([300], 16, 2, 64, dtype)
+    q = randn(1, 1, Hq, 64, dtype=dtype)
+    q[:, :, 3] = q[:, :, 3].abs() + 0.5
+    for j in (7, 250):
+        c.k_pages[0, int(c.block_table[0, j // 16]), j % 16, :, 3] = -float("inf")
+    keep = [j for j in range(300) if j not in (7, 250)]
+    o, lse = lcx.paged_decode(c, q, ints([0]), rope, prerotated=True, return_lse=True)
+    rows = [tuple(x[keep] for x in rows[0])]
+    want = plain_decode(q, rows, [298], [0], rope, prerotated=True)
+    check_decode(o, lse, want, dtype, Hq // 2, 300)

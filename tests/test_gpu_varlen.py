@@ -438,3 +438,25 @@ def test_rows_of_a_foreign_plan_are_left_out_and_reported(dt):
     assert (out[100:] == 5).all() and (lse[:, 100:] == 5).all()
     compare(out[:100], lse[:, :100], plain(q[:100], k[:100], v[:100], [100], [100], rope), dtype,
             100)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_a_visible_key_at_minus_infinity_weighs_nothing(dt):
+    """A logit of -inf (an infinite key, given rotated) has the weight 0, a logit of
+    +inf makes the row NaN."""
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    rope = lcx.RopeParams("plain", 64)
+    n = 150
+    q, k, v = (randn(i, n, h, 64, dtype=dtype) for i, h in ((1, 4), (2, 2), (3, 2)))
+    q[:, :, 3] = q[:, :, 3].abs() + 0.5
+    k[[7, 90], :, 3] = -float("inf")
+    keep = [j for j in range(n) if j not in (7, 90)]
+    o, lse = lcx.attn_varlen(q, k, v, lcx.VarlenPlan([n]), rope, causal=False, prerotated=True,
+                             return_lse=True)
+    want = plain(q, k[keep], v[keep], [n], [n - 2], rope, causal=False, prerotated=True)
+    compare(o, lse, want, dtype, n)
+    k[20, 1, 3] = float("inf")
+    o2, lse2 = lcx.attn_varlen(q, k, v, lcx.VarlenPlan([n]), rope, causal=False, prerotated=True,
+                               return_lse=True)
+    assert torch.equal(o2[:, :2], o[:, :2]) and torch.equal(lse2[:2], lse[:2])
+    assert torch.isnan(o2[:, 2:].float()).all() and torch.isnan(lse2[2:]).all()
