@@ -616,8 +616,9 @@ typedef struct {
  *   Supported: D 64 or 128, full rotary; o does not overlap k or v; bf16: no
  *   stride of 0.
  *   Arithmetic: bf16: tensor-core products with fp32 accumulation; q' and k'
- *   rounded to fp16 (rows out of its range scaled by a power of two), in two fp16
- *   parts for row blocks that start before position 127 or see fewer keys; given
+ *   rounded to fp16 (rows whose largest value leaves [2^-6, 2^14) are scaled to just
+ *   below 2^14 by a power of two; values below 2^-14 then keep steps of 2^-24), in two
+ *   fp16 parts for row blocks that start before position 127 or see fewer keys; given
  *   rotated inputs enter as they are; the weights rounded to bf16, their sum not.
  *   fp32: every operand of a product as two tf32 parts (within 2^-21 of it).
  *   dev_status: LCX_ERR_TIMEOUT after an expired wait, as lcx_attn_fwd (o and lse

@@ -413,12 +413,14 @@ struct KeyParams {
     double theta[64];
 };
 
-// Power of two near 1 / amax when amax leaves [2^-6, 2^14), else 1; *undo its
-// reciprocal.  (bf16 values reach 2^128: the exponent is kept below 126.)
+// The power of two that brings amax to [2^13, 2^14) when it leaves [2^-6, 2^14), else 1;
+// *undo its reciprocal.  (fp16 keeps 11 bits down to 2^-14 and steps of 2^-24 below: the
+// top of its range leaves most room for a row's small values.  fp32 and bf16 values reach
+// from 2^-133 to 2^128: powers up to 2^125, so that both are normal numbers.)
 __device__ __forceinline__ float range_scale(float amax, float *undo) {
     *undo = 1.f;
     if ((amax >= 0.015625f && amax < 16384.f) || amax == 0.f || !(amax < INFINITY)) return 1.f;
-    const int e = min(max(int(__float_as_uint(amax) >> 23) - 127, -125), 125);
+    const int e = max(int(__float_as_uint(amax) >> 23) - 127 - 13, -125);
     *undo = __uint_as_float(uint32_t(127 + e) << 23);
     return __uint_as_float(uint32_t(127 - e) << 23);
 }
@@ -858,9 +860,10 @@ __device__ __forceinline__ bool keys_scaled(const TcParams &p, const Block &b, i
     return any;
 }
 
-// Multiply a row's scores of key tile jt (TMEM, from taddr on) by the keys' scales.
+// Multiply a row's scores of key tile jt (TMEM, from taddr on) by the keys' scales and the
+// query's, their product first: keys at one end of the exponents meet queries at the other.
 __device__ __noinline__ void scale_scores(const TcParams &p, const Block &b, uint32_t taddr,
-                                          int jt) {
+                                          int jt, float q_scale) {
     const int last = b.u.nk - jt * kBN;
     const float *ks = p.k_scale + (long long)(b.u.k0 + jt * kBN) * p.v.Hkv + b.g;
 #pragma unroll 1
@@ -871,7 +874,7 @@ __device__ __noinline__ void scale_scores(const TcParams &p, const Block &b, uin
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
             const float f = c + e < last ? ks[(long long)(c + e) * p.v.Hkv] : 1.f;
-            u[e] = __float_as_uint(x[e] * f);
+            u[e] = __float_as_uint(x[e] * (f * q_scale));
         }
         tmem_st32(taddr + c, u);
     }
@@ -1204,12 +1207,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n = B.n;
             const uint32_t trow = tmem + (uint32_t((warp & 3) * 32) << 16);
             const uint32_t s_col = t * kBN, o_col = C::kColO + t * D;
+            auto q_scale = [&]() {
+                return __uint_as_float(uint32_t(127 + bar.q_exp[t * kBM + row]) << 23);
+            };
             float m = -INFINITY, l = 0.f, cl2 = v.c_log2;
             bool scaled = false;
             if (p.fp16 && n > 0 && ok) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&bar.ready_q, 0, abort, tmo));
-                cl2 *= __uint_as_float(uint32_t(127 + bar.q_exp[t * kBM + row]) << 23);
                 scaled = bar.k_scaled != 0;
+                if (!scaled) cl2 *= q_scale();
             }
             for (int j = 0; ok && j < n; ++j) {
                 const int jt = B.tile(j);
@@ -1217,7 +1223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __all_sync(0xffffffffu, mbar_wait(&bar.s_ready[t], j & 1, abort, tmo));
                 if (!ok) break;
                 tc_fence_after();
-                if (scaled) scale_scores(p, B, trow + s_col, jt);
+                if (scaled) scale_scores(p, B, trow + s_col, jt, q_scale());
                 float x[kBN];
                 tmem_ld128(trow + s_col, x);
                 if (!whole) {

@@ -460,3 +460,44 @@ def test_a_visible_key_at_minus_infinity_weighs_nothing(dt):
                                return_lse=True)
     assert torch.equal(o2[:, :2], o[:, :2]) and torch.equal(lse2[:2], lse[:2])
     assert torch.isnan(o2[:, 2:].float()).all() and torch.isnan(lse2[2:]).all()
+
+
+@pytest.mark.parametrize("Hq,H,D", [(4, 2, 128), (3, 1, 64)])
+@pytest.mark.parametrize("up,down", [(500.0, 1.0), (8000.0, 2.0 ** -8), (2000.0, 2.0 ** -13)])
+def test_rows_with_outlier_channels(Hq, H, D, up, down):
+    """Rows of q and k with a few channels far above the others, not the same ones, so the
+    logits come from the products of both sizes.  Bound: besides fp16's relative
+    rounding, values below 2^-14 (after a row's scaling by a power of two, which makes its
+    largest value at least 2^-6) keep an absolute one of 2^-25; a logit moves by c
+    (|q'|_1 + |k'|_1) 2^-25 for it, in units of rows whose largest value is below 2^14."""
+    rope = lcx.RopeParams("plain", D)
+    lens = [130, 300, 7]
+    n = sum(lens)
+    q, k, v = (randn(i, n, h, D, dtype=torch.float32) for i, h in ((1, Hq), (2, H), (3, H)))
+    q, k = q * down, k * down
+    q[:, :, [3, D // 2 + 9]] *= up / down / 8
+    k[:, :, [5, D - 2]] *= up / down
+    q, k, v = (x.bfloat16() for x in (q, k, v))
+    o, lse = lcx.attn_varlen(q, k, v, lcx.VarlenPlan(lens), rope, return_lse=True)
+    w = plain(q, k, v, lens, lens, rope)
+    u_s, u_p = arithmetic(torch.bfloat16, 300)
+    # |q'|_1 <= sqrt(2) |q|_1, and scaled rows' floors are 2^-25 of the row's power of two
+    def floor(x):
+        mx = (2.0 ** 0.5) * x.float().abs().amax(-1)
+        return torch.exp2(torch.floor(torch.log2(torch.clamp(mx / 2.0 ** 14, min=1.0))) - 24)
+    f = max(float(floor(q).max()), float(floor(k).max()))
+    one = 2.0 ** 0.5 * max(float(x.float().abs().sum(-1).max()) for x in (q, k))
+    extra = D ** -0.5 * 2 * one * f
+    check(o, lse, (w[0], w[1], w[2], w[3] + extra / u_s), u_s, u_p, "outliers %g %g" % (up, down))
+
+
+@pytest.mark.parametrize("Hq,H,D", [(4, 2, 128), (3, 1, 64)])
+@pytest.mark.parametrize("e", [60, 115, 122, -122])
+def test_queries_and_keys_at_opposite_ends_of_the_exponents(e, Hq, H, D):
+    """Rows of q about 2^-e, rows of k about 2^e: ordinary logits."""
+    rope = lcx.RopeParams("plain", D)
+    lens = [200, 333]
+    q, k, v = (randn(i, 533, h, D) for i, h in ((1, Hq), (2, H), (3, H)))
+    q, k = (q.double() * 2.0 ** -e).bfloat16(), (k.double() * 2.0 ** e).bfloat16()
+    o, lse = lcx.attn_varlen(q, k, v, lcx.VarlenPlan(lens), rope, return_lse=True)
+    compare(o, lse, plain(q, k, v, lens, lens, rope), torch.bfloat16, 333)
