@@ -916,17 +916,20 @@ lcx_status launch_decode(DecodeParams &p, cudaStream_t s) {
     using C = Dec<T, D, kWide>;
     p.blk = C::BLK;
     auto kern = paged_decode_kernel<T, D, kWide>;
+    const long long segments = (long long)p.n * p.Hkv * p.hb;
+    if (segments > 0x7fffffffLL) return fail(LCX_ERR_UNSUPPORTED, "sizes too large");
+    // no more CTAs than blocks there can be: a sequence's, and what the visible keys'
+    // places add under a window (less than kAlign before lo and behind the sinks); the
+    // kernels count the blocks of all entries in 32 bits
+    const long long places = ((long long)p.MP << p.ps_log2) + (p.window > 0 ? 2 * kAlign : 0);
+    const long long most = places / p.blk + 1;
+    if (most * p.n > 0x7fffffffLL)
+        return fail(LCX_ERR_UNSUPPORTED, "too many entries for sequences of this length");
+    p.ctas = int(std::min<long long>(p.ctas, segments * most));
     cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess)
         return fail(LCX_ERR_CUDA, "cudaFuncSetAttribute failed: %s", cudaGetErrorString(e));
-    const long long segments = (long long)p.n * p.Hkv * p.hb;
-    if (segments > 0x7fffffffLL) return fail(LCX_ERR_UNSUPPORTED, "sizes too large");
-    // no more CTAs than blocks there can be
-    const long long most = ((long long)p.MP << p.ps_log2) / p.blk + 1;
-    if (most * p.n > 0x7fffffffLL)
-        return fail(LCX_ERR_UNSUPPORTED, "too many entries for sequences of this length");
-    p.ctas = int(std::min<long long>(p.ctas, segments * most));
     e = launch_dependent(kern, dim3(unsigned(p.ctas)), dim3(kThreads), C::kSmem, s, p);
     if (e == cudaSuccess && p.ctas > 1)
         e = launch_dependent(join_kernel<T, D, C::HB>, dim3(unsigned(segments)), dim3(kThreads), 0,

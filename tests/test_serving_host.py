@@ -367,3 +367,13 @@ def test_plain_pages_hold_their_invariants():
                 assert m.ref[pages[-1]] == 1
         assert held == m.ref
         assert sorted(m.free) == [p for p in range(40) if m.ref[p] == 0]
+
+
+def test_decode_refuses_more_blocks_than_an_int_counts(lib):
+    """2^20 entries of up to 65503 fp32 keys, D 128: blocks of 32 keys, 2047 of them; a
+    window and sinks that begin inside a block add up to two more, and the blocks of all
+    entries are counted in 32 bits."""
+    c = cache_args(dtype=1, D=128, Hkv=1, page_size=1, max_pages=65503, num_pages=1 << 20)
+    a = decode_args(n=1 << 20, Hq=1, window=65472, sinks=31)
+    need = lib.lcx_paged_decode_workspace_bytes(1 << 20, 1, 1, 128)
+    assert lib.lcx_paged_decode(ctypes.byref(c), ctypes.byref(a), F, need, None) == UNS
