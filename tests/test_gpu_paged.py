@@ -561,3 +561,69 @@ def test_decode_key_at_minus_infinity_weighs_nothing(dt, Hq):
     rows = [tuple(x[keep] for x in rows[0])]
     want = plain_decode(q, rows, [298], [0], rope, prerotated=True)
     check_decode(o, lse, want, dtype, Hq // 2, 300)
+
+
+def counted(lens, ps, H, D, dtype, unit):
+    """A cache whose keys count for the same (q = 0) and whose values say which run of
+    `unit` keys they belong to: column (j // unit) mod D is 1, the others 0.  With it,
+    per sequence, how often each column's 1 occurs."""
+    c, _ = cache_of(lens, ps, H, D, dtype)
+    counts = []
+    for s, n in enumerate(lens):
+        pos = torch.arange(n, device="cuda")
+        col = (pos // unit) % D
+        pg, sl = c.block_table[s].long()[pos // ps], pos % ps
+        c.v_pages[0, pg, sl] = torch.eye(D, device="cuda", dtype=dtype)[col][:, None]
+        counts.append(torch.bincount(col.cpu(), minlength=D).double())
+    return c, counts
+
+
+@pytest.mark.parametrize("lens,H,Hq,D", [
+    ([70001], 1, 3, 64), ([70001], 1, 12, 64), ([70001], 1, 2, 128),
+    ([30000, 5, 0, 12345, 64, 8191], 2, 8, 128), ([9000] * 7 + [1], 3, 60, 64),
+    ([200000], 1, 20, 128), ([257] * 40, 4, 4, 64)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_decode_joins_every_key_once(lens, H, Hq, D, dt):
+    """Equal weights: lse is the logarithm of the number of keys and o the share of every
+    run of 48 keys.  A lost or doubled part, block or tile (8 keys and more of a run)
+    moves both far beyond the rounding: the weights are 1, all sums are whole numbers
+    below 2^24, so o carries 1/z, a product and the output's rounding, lse a logarithm
+    and a product."""
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    c, counts = counted(lens, 64, H, D, dtype, 48)
+    q = torch.zeros((len(lens), Hq, D), dtype=dtype, device="cuda")
+    o, lse = lcx.paged_decode(c, q, ints(list(range(len(lens)))), lcx.RopeParams("plain", D),
+                              return_lse=True)
+    for s, n in enumerate(lens):
+        if n == 0:
+            assert (o[s] == 0).all() and (lse[s] == -float("inf")).all()
+            continue
+        want = counts[s] / n
+        assert ((o[s].double().cpu() - want).abs() <= (U_OUT[dtype] + 2.0 ** -22) * want).all()
+        wl = float(torch.log(torch.tensor(n).double()))
+        assert (lse[s].double().cpu() - wl).abs().max() <= 2.0 ** -21 * (1 + wl)
+
+
+@pytest.mark.parametrize("Hq", [3, 12])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_decode_long_sequence_within_its_chained_sums(Hq, dt):
+    """A sequence over every CTA against the 64-bit form, the sums bounded by what the
+    kernel chains: a warp's quarter of a stretch (two CTAs an SM share the keys, in blocks
+    of at most 128), four warps, and the parts, which lanes of a warp add (10 and 5
+    steps).  Half a CTA's keys missing would move lse by 1.7e-3, beyond its bound."""
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    n, D = 70001, 64
+    rope = lcx.RopeParams("plain", D)
+    c, rows = cache_of([n], 64, 1, D, dtype)
+    q = (0.5 * randn(2, 1, Hq, D, dtype=torch.float32)).to(dtype)
+    o, lse = lcx.paged_decode(c, q, ints([0]), rope, return_lse=True)
+    ctas = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    chain = (n // ctas + 2 * 128) // 4 + 4 + 15
+    wo, wl, wm, wp = plain_decode(q, rows, [n], [0], rope)
+    check_decode(o, lse, (wo, wl, wm, wp), dtype, Hq, chain)
+    u_s, u_p = arithmetic(dtype, Hq, chain)
+    if Hq > 8 and dtype == torch.bfloat16:
+        u_p -= 2.0 ** -8                   # lse sums the weights before their rounding
+    bound = u_s * wp + 2.0 ** -22 * (1 + wl.abs()) + u_p
+    assert float(bound.max()) <= 1e-3
+    assert ((lse.double().cpu() - wl).abs() <= bound).all()
