@@ -501,3 +501,85 @@ def test_queries_and_keys_at_opposite_ends_of_the_exponents(e, Hq, H, D):
     q, k = (q.double() * 2.0 ** -e).bfloat16(), (k.double() * 2.0 ** e).bfloat16()
     o, lse = lcx.attn_varlen(q, k, v, lcx.VarlenPlan(lens), rope, return_lse=True)
     compare(o, lse, plain(q, k, v, lens, lens, rope), torch.bfloat16, 333)
+
+
+# Packed keys beyond 80 MiB take the CTA order by kv head: two heads a CTA, two row
+# blocks a CTA (odd groups), one tile a CTA (few row blocks).
+LONG = [([4000, 1300], [4000, 1300], 8, 2, 128, "bf16"),
+        ([200, 3, 300], [9000, 6000, 6001], 64, 8, 128, "bf16"),
+        ([200, 3, 300], [9000, 6000, 6001], 40, 8, 128, "bf16"),
+        ([40, 130], [15000, 6001], 16, 8, 128, "bf16"),
+        ([70, 300], [36000, 6001], 8, 8, 64, "bf16"),
+        ([33, 130], [5000, 1000], 4, 2, 128, "f32"),
+        ([33, 130], [5000, 1000], 3, 1, 64, "f32")]
+
+
+@pytest.mark.parametrize("lq,lk,Hq,H,D,dt", LONG)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (2500, 200)])
+def test_long_rows_see_every_key_once(lq, lk, Hq, H, D, dt, window, sinks):
+    """Equal weights (q = 0) and values that say which run of 48 keys, of which sequence
+    and kv head, they belong to: o is the share of every run, lse the logarithm of the
+    number of keys.  A lost, doubled or foreign tile moves both far beyond the rounding:
+    the weights are 1 (or a power of two), all sums whole numbers below 2^24, so o
+    carries 1/z, a product and the output's rounding, lse a logarithm and a product."""
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    rope = lcx.RopeParams("plain", D)
+    q = torch.zeros((sum(lq), Hq, D), dtype=dtype, device="cuda")
+    k = randn(2, sum(lk), H, D, dtype=dtype)
+    v = torch.zeros_like(k)
+    eye = torch.eye(D, dtype=dtype, device="cuda")
+    at, cols = 0, []
+    for s, n in enumerate(lk):
+        cols.append([(torch.arange(n, device="cuda") // 48 + 5 * s + 11 * g) % D for g in range(H)])
+        for g in range(H):
+            v[at:at + n, g] = eye[cols[s][g]]
+        at += n
+    o, lse = lcx.attn_varlen(q, k, v, lcx.VarlenPlan(lq, lk), rope, window=window, sinks=sinks,
+                             return_lse=True)
+    at = 0
+    for s, (n, m) in enumerate(zip(lq, lk)):
+        pos, key = torch.arange(n, device="cuda") + (m - n), torch.arange(m, device="cuda")
+        keep = key[None, :] <= pos[:, None]
+        if window:
+            keep &= (pos[:, None] - key[None, :] < window) | (key[None, :] < sinks)
+        z = keep.sum(1).double()
+        for g in range(H):
+            want = (keep.double() @ eye[cols[s][g]].double()) / z[:, None]
+            r = slice(g * (Hq // H), (g + 1) * (Hq // H))
+            err = (o[at:at + n, r].double() - want[:, None]).abs()
+            u = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
+            assert (err <= (u + 2.0 ** -22) * want[:, None]).all()
+        wl = torch.log(z)
+        assert ((lse[:, at:at + n].double() - wl).abs() <= 2.0 ** -21 * (1 + wl)).all()
+        at += n
+
+
+@pytest.mark.parametrize("lq,lk,Hq,H,D,dt", LONG)
+def test_long_rows_find_their_key(lq, lk, Hq, H, D, dt):
+    """Every query looks for one key anywhere in its past (q' = 3 k' there, a logit of
+    some 3 sqrt(D) among N(0, 9) ones), so o is nearly that key's value: within the bounds
+    of the 64-bit form, on every eleventh row."""
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    rope = lcx.RopeParams("plain", D)
+    k, v = (randn(i, sum(lk), H, D, dtype=dtype) for i in (2, 3))
+    g = torch.Generator().manual_seed(7)
+    q = torch.empty((sum(lq), Hq, D), dtype=dtype, device="cuda")
+    rows, a, b = [], 0, 0
+    kc = k.double().cpu()
+    for n, m in zip(lq, lk):
+        pos = torch.arange(n) + (m - n)
+        for h in range(Hq):
+            t = (torch.rand(n, generator=g) * (pos + 1)).long()
+            # R(p) q = 3 R(t) k
+            x = rotate(kc[b + t, h // (Hq // H)][:, None], t - pos, rope)
+            q[a:a + n, h] = (3 * x[:, 0]).to(dtype).cuda()
+        rows.append((torch.arange(0, n, 11), a, b, n, m))
+        a, b = a + n, b + m
+    o, lse = lcx.attn_varlen(q, k, v, lcx.VarlenPlan(lq, lk), rope, return_lse=True)
+    for r, a, b, n, m in rows:
+        pos = r + (m - n)
+        qs = rotate(q[a + r.cuda()].cpu(), pos, rope)
+        ks = rotate(k[b:b + m].cpu(), torch.arange(m), rope)
+        want = attend(qs, ks, v[b:b + m].double().cpu(), pos, True, 0, 0, D ** -0.5)
+        assert float(want[0].abs().mean()) > 0.5
+        check(o[a + r.cuda()], lse[:, a + r.cuda()], want, *arithmetic(dtype, m), "%d of %d" % (n, m))
