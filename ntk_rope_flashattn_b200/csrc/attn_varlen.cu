@@ -1488,10 +1488,20 @@ lcx_status run_tc(const lcx_varlen_args *a, const VarlenParams &v, cudaStream_t 
     p.v = v;
     p.fp16 = rotate ? 1 : 0;
     p.stall = (a->flags & LCX_VARLEN_TEST_STALL) ? 1 : 0;
-    // Two query tiles per CTA when those CTAs still cover the SMs; a problem of few
-    // row blocks runs faster over twice the CTAs, one tile each.
-    const int64_t pairs = v.G % 2 == 0 ? I.n_units[0] * (v.Hq / 2) : I.n_units[1] * v.Hq;
-    p.mode = pairs < device_sms() ? kOneTile : v.G % 2 == 0 ? kTwoHeads : kTwoBlocks;
+    // Two query tiles per CTA, unless CTAs of one tile each fit the SMs at once (1 x 512
+    // tokens of 32/8 heads of 128: one tile 21.3, two 22.9 us; 5 x 128: 26.9 and 18.7; 640
+    // behind 8000 keys: 250 and 157; 4096 of 8/2 heads of 64 under a window of 300: 32.1
+    // and 22.8).  Causal prompts of 1500 tokens and more are uneven enough for one tile as
+    // long as the CTAs of two leave SMs idle (3500 of 8/2 heads of 64: 57.7 and 63.8; 2000
+    // of 12/4 heads of 128: 43.2 and 49.2).
+    const int64_t one = I.n_units[0] * v.Hq;
+    const int64_t pairs = v.G % 2 == 0 ? one / 2 : I.n_units[1] * v.Hq;
+    const bool uneven = v.causal && v.window == 0 && I.total_q == I.total_k &&
+                        I.total_q >= 1500 * I.n_seqs;
+    const int sms = device_sms();
+    p.mode = one <= sms || (uneven && pairs < sms) ? kOneTile
+             : v.G % 2 == 0                        ? kTwoHeads
+                                                   : kTwoBlocks;
     p.group_units = p.mode == kTwoHeads ? v.G / 2 : v.G;
     // Order of the CTAs.  All heads of the heaviest row blocks first balances best;
     // when the keys and values of all heads exceed what L2 holds for both dies, kv head
