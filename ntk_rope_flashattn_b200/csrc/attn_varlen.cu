@@ -1503,12 +1503,15 @@ lcx_status run_tc(const lcx_varlen_args *a, const VarlenParams &v, cudaStream_t 
              : v.G % 2 == 0                        ? kTwoHeads
                                                    : kTwoBlocks;
     p.group_units = p.mode == kTwoHeads ? v.G / 2 : v.G;
-    // Order of the CTAs.  All heads of the heaviest row blocks first balances best;
-    // when the keys and values of all heads exceed what L2 holds for both dies, kv head
-    // by kv head reads them from there instead (15.8k tokens of 8 heads, 65 MB: 384
-    // against 401 us; 16.4k, 67 MB: the same; 26k, 107 MB: 2734 against 2626 us; 32.8k:
-    // 8955 against 8715 us).
-    p.by_head = I.total_k * v.Hkv * a->D * 4 > (int64_t(80) << 20);
+    // Order of the CTAs.  All heads of the heaviest row blocks first balances best.  When
+    // the keys and values of all heads exceed what L2 holds for both dies, kv head by kv
+    // head reads them from there instead, and the power saved goes into the clock: on a GPU
+    // kept busy 12 x 4096 tokens of 32/8 heads of 128 take 2147 against 2313 us, 2 x 26000
+    // 11.7 against 12.1 ms, 1 x 32768 9.13 against 9.30, 32 x 1024 585 against 613 us (64 x
+    // 512: 465 and 460; after a pause, at full clock, it costs up to 2 %: 2099 and 2075).
+    // Heads of 64 and groups of one do not gain: 32 x 1024 tokens of 32/16 heads of 64 504
+    // against 470 us, 22000 of 8/8 heads of 128 1184 against 1119.
+    p.by_head = a->D == 128 && v.G > 1 && I.total_k * v.Hkv * a->D * 4 > (int64_t(80) << 20);
     const int which = p.mode == kTwoBlocks;
     p.v.units =
         reinterpret_cast<const VarlenUnit *>(a->plan + plan_units(I.n_seqs, which, I.n_units[0]));

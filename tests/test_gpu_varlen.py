@@ -503,8 +503,8 @@ def test_queries_and_keys_at_opposite_ends_of_the_exponents(e, Hq, H, D):
     compare(o, lse, plain(q, k, v, lens, lens, rope), torch.bfloat16, 333)
 
 
-# Packed keys beyond 80 MiB take the CTA order by kv head: two heads a CTA, two row
-# blocks a CTA (odd groups), one tile a CTA (few row blocks).
+# Packed keys beyond 80 MiB take the CTA order by kv head (heads of 128, groups of two and
+# more): two heads a CTA, two row blocks a CTA (odd groups), one tile a CTA (few row blocks).
 LONG = [([4000, 1300], [4000, 1300], 8, 2, 128, "bf16"),
         ([200, 3, 300], [9000, 6000, 6001], 64, 8, 128, "bf16"),
         ([200, 3, 300], [9000, 6000, 6001], 40, 8, 128, "bf16"),
@@ -583,3 +583,37 @@ def test_long_rows_find_their_key(lq, lk, Hq, H, D, dt):
         want = attend(qs, ks, v[b:b + m].double().cpu(), pos, True, 0, 0, D ** -0.5)
         assert float(want[0].abs().mean()) > 0.5
         check(o[a + r.cuda()], lse[:, a + r.cuda()], want, *arithmetic(dtype, m), "%d of %d" % (n, m))
+
+
+@pytest.mark.parametrize("Hq,H,D", [(16, 8, 128), (32, 16, 64)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (4000, 300)])
+def test_long_prompts_see_every_key_once(Hq, H, D, window, sinks):
+    """Prompts of 123 MiB of keys and values (with heads of 128 in the CTA order by kv
+    head): equal weights over values that say which run of 240 keys, of which sequence and
+    kv head, they belong to, on rows all over the prompts (bounds:
+    test_long_rows_see_every_key_once)."""
+    lens = [17000, 14500]
+    rope = lcx.RopeParams("plain", D)
+    q = torch.zeros((sum(lens), Hq, D), dtype=torch.bfloat16, device="cuda")
+    k = randn(2, sum(lens), H, D)
+    eye = torch.eye(D, dtype=torch.bfloat16, device="cuda")
+    cols = [[(torch.arange(n, device="cuda") // 240 + 5 * s + 11 * g) % D for g in range(H)]
+            for s, n in enumerate(lens)]
+    v = torch.stack([torch.cat([eye[cols[s][g]] for s in range(2)]) for g in range(H)], 1)
+    o, lse = lcx.attn_varlen(q, k, v, lcx.VarlenPlan(lens), rope, window=window, sinks=sinks,
+                             return_lse=True)
+    at = 0
+    for s, n in enumerate(lens):
+        pos = torch.cat([torch.arange(0, n, 37), torch.arange(n - 200, n)]).cuda()
+        key = torch.arange(n, device="cuda")
+        keep = key[None, :] <= pos[:, None]
+        if window:
+            keep &= (pos[:, None] - key[None, :] < window) | (key[None, :] < sinks)
+        z, keep = keep.sum(1).double(), keep.double()
+        for g in range(H):
+            want = (keep @ eye[cols[s][g]].double()) / z[:, None]
+            got = o[at + pos, g * (Hq // H):(g + 1) * (Hq // H)].double()
+            assert ((got - want[:, None]).abs() <= (2.0 ** -8 + 2.0 ** -22) * want[:, None]).all()
+        wl = torch.log(z)
+        assert ((lse[:, at + pos].double() - wl).abs() <= 2.0 ** -21 * (1 + wl)).all()
+        at += n
