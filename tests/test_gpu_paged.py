@@ -627,3 +627,52 @@ def test_decode_long_sequence_within_its_chained_sums(Hq, dt):
     bound = u_s * wp + 2.0 ** -22 * (1 + wl.abs()) + u_p
     assert float(bound.max()) <= 1e-3
     assert ((lse.double().cpu() - wl).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_pages_far_apart_in_memory(dt):
+    """Pages more than 2^32 bytes and 2^31 elements apart: append, decode, fork, page copy
+    and compaction equal the same calls on a dense cache."""
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    P, ps, H, D = 6, 4, 2, 64
+    stride = (1 << 29) + 64
+    rope = lcx.RopeParams("plain", D)
+    big = [torch.empty(5 * stride + ps * H * D, dtype=dtype, device="cuda") for _ in range(2)]
+    far = [t.as_strided((1, P, ps, H, D), (0, stride, H * D, D, 1)) for t in big]
+    assert 5 * stride > 2 ** 31 and 5 * stride * big[0].element_size() > 2 ** 32
+    a = lcx.PagedCache(P, ps, H, D, 3, 6, dtype=dtype, k_pages=far[0], v_pages=far[1])
+    b = lcx.PagedCache(P, ps, H, D, 3, 6, dtype=dtype)
+    k, v = randn(1, 10, H, D, dtype=dtype), randn(2, 10, H, D, dtype=dtype)
+    q = randn(3, 3, 4, D, dtype=dtype)
+    for c in (a, b):
+        c.k_pages.zero_()
+        c.v_pages.zero_()
+    got = []
+    for c in (a, b):
+        ids = ints([0, 1])
+        c.free_pages.copy_(ints([4, 3, 1, 5, 0, 2]))    # sequence 0 takes 5 and 0, 1 takes 2
+        start = lcx.pages_extend(c, ids, ints([7, 3]))
+        lcx.paged_append(c, k, v, ids, start, rope, cu_new=ints([0, 7, 10]))
+        lcx.pages_fork(c, ints([0]), ints([2]))
+        one = lcx.paged_decode(c, q, ints([0, 1, 2]), rope)
+        lcx.pages_free(c, ints([1]))
+        lcx.pages_compact(c)                            # 5 -> 2
+        assert c.block_table[0, :2].tolist() == [2, 0]
+        two = lcx.paged_decode(c, q, ints([0, 1, 2]), rope)
+        lcx.pages_copy(c, ints([0]), ints([5]))
+        got.append((one, two, c.meta.clone(), c.k_pages.clone(), c.v_pages.clone()))
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    assert torch.equal(got[0][0][[0, 2]], got[0][1][[0, 2]])
+
+
+@pytest.mark.parametrize("Hq", [8, 24])
+def test_decode_in_place(Hq):
+    """out = q: a query is read before its row is written, whole or joined."""
+    lens = [3000, 40, 0, 700]
+    rope = lcx.RopeParams("plain", 128)
+    c, _ = cache_of(lens, 16, 2, 128)
+    q = randn(4, 4, Hq, 128)
+    want = lcx.paged_decode(c, q, ints([0, 1, 2, 3]), rope)
+    assert torch.equal(lcx.paged_decode(c, q, ints([0, 1, 2, 3]), rope, out=q), want)
+    assert torch.equal(q, want)

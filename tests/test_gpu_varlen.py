@@ -617,3 +617,54 @@ def test_long_prompts_see_every_key_once(Hq, H, D, window, sinks):
         wl = torch.log(z)
         assert ((lse[:, at + pos].double() - wl).abs() <= 2.0 ** -21 * (1 + wl)).all()
         at += n
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_rows_far_apart_in_memory(dt):
+    """Tokens 2^24 bytes apart and more, in all more than 2^31 elements: equal to the packed call."""
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    lens, D = [150, 130], 64
+    T, stride = 280, (1 << 23) + 64
+    rope = lcx.RopeParams("plain", D)
+    plan = lcx.VarlenPlan(lens)
+    q, k, v = (randn(i, T, h, D, dtype=dtype) for i, h in ((1, 4), (2, 2), (3, 2)))
+    want, wl = lcx.attn_varlen(q, k, v, plan, rope, return_lse=True)
+    big = torch.empty((T - 1) * stride + 12 * D, dtype=dtype, device="cuda")
+    assert big.numel() > 2 ** 31
+    at, far = 0, []
+    for t in (q, k, v, want):
+        x = big.as_strided(t.shape, (stride, D, 1), at)
+        x.copy_(t)
+        far.append(x)
+        at += t.shape[1] * D
+    far[3].fill_(7)
+    o, lse = lcx.attn_varlen(*far[:3], plan, rope, return_lse=True, out=far[3])
+    assert torch.equal(o, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("lens", [[300, 7, 129], [64] * 40])
+@pytest.mark.parametrize("Hq,H,dt", [(8, 2, "bf16"), (9, 3, "bf16"), (4, 2, "f32")])
+def test_output_over_the_queries(lens, Hq, H, dt):
+    """out = q (o does not overlap k or v, but may take q's place)."""
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    rope = lcx.RopeParams("plain", 64)
+    plan, T = lcx.VarlenPlan(lens), sum(lens)
+    q, k, v = (randn(i, T, h, 64, dtype=dtype) for i, h in ((1, Hq), (2, H), (3, H)))
+    want = lcx.attn_varlen(q, k, v, plan, rope)
+    for prerotated in (False, True):
+        x = q.clone()
+        w = lcx.attn_varlen(x, k, v, plan, rope, prerotated=prerotated)
+        assert torch.equal(lcx.attn_varlen(x, k, v, plan, rope, prerotated=prerotated, out=x), w)
+        assert prerotated or torch.equal(x, want)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_queries_without_any_key(dt):
+    """No sequence has a key: o = 0, lse = -inf, causal or not."""
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    rope = lcx.RopeParams("plain", 64)
+    q, k = randn(1, 140, 4, 64, dtype=dtype), randn(2, 0, 2, 64, dtype=dtype)
+    for causal in (True, False):
+        o, lse = lcx.attn_varlen(q, k, k, lcx.VarlenPlan([130, 0, 10], [0, 0, 0]), rope,
+                                 causal=causal, return_lse=True)
+        assert (o == 0).all() and (lse == -float("inf")).all()
