@@ -438,8 +438,9 @@ LCX_API lcx_status lcx_pages_extend(const lcx_paged_cache *cache, const int32_t 
  * to a page from the free stack (the block rule of lcx_pages_extend).  All
  * sources are read as they were before the call; one source may be forked
  * several times.  Skipped: a negative src or dst; with a status: a number >=
- * max_seqs, a dst that is not empty or seen earlier (LCX_ERR_INVALID_ARG),
- * entries without a free page (LCX_ERR_NO_PAGES).
+ * max_seqs, a dst that is not empty or stands in an earlier entry, a skipped one
+ * included (LCX_ERR_INVALID_ARG: pad both with a negative number), entries without a
+ * free page (LCX_ERR_NO_PAGES).
  */
 LCX_API lcx_status lcx_pages_fork(const lcx_paged_cache *cache, const int32_t *src,
                                   const int32_t *dst, int64_t n, int32_t *dev_status,
@@ -467,7 +468,8 @@ LCX_API lcx_status lcx_pages_compact(const lcx_paged_cache *cache, int32_t *dev_
  * bookkeeping is not touched.  Skipped with LCX_ERR_INVALID_ARG: a number
  * outside [0, num_pages), a destination seen earlier or that is also a source
  * of the call (a page copied to itself is left alone without a status); a
- * negative source or destination is skipped silently.
+ * negative source or destination is skipped silently.  Skipped entries count among
+ * the earlier ones and the sources: pad both with a negative number.
  */
 LCX_API lcx_status lcx_pages_copy(const lcx_paged_cache *cache, const int32_t *src_pages,
                                   const int32_t *dst_pages, int64_t n, int32_t *dev_status,
@@ -559,7 +561,7 @@ typedef struct {
 } lcx_varlen_info;
 
 /* int32 values of a plan for n sequences (-1: a negative length, or sums of
- * 2^30 tokens and more).  Host only. */
+ * more than 2^30 tokens).  Host only. */
 LCX_API int64_t lcx_varlen_plan_ints(const int32_t *lens_q, const int32_t *lens_k, int64_t n);
 
 /*

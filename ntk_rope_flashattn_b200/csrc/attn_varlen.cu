@@ -29,7 +29,7 @@
 // Operands of QK^T.  Rotated values are not bf16 numbers, and a logit's rounding
 // error reaches lse unweakened when a row sees few keys.  q' and k' are therefore
 // fp16 (11 bits instead of 8, the same tensor-core rate), each row scaled by a power
-// of two when its largest value leaves fp16's comfortable range (rows scale c; scaled
+// of two when its largest value leaves [2^-6, 2^14) (a query's power goes into c; scaled
 // keys, rare, take a slower path), and row blocks that start before position 127, or
 // see fewer keys, add the products with the operands' fp16 remainders ("precise":
 // their few key tiles cost three products instead of one).  Given rotated inputs

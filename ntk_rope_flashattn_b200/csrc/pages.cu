@@ -6,7 +6,7 @@
 // prefix sums, so results do not depend on thread order), and a second kernel,
 // a programmatic dependent, moves the data: page copies are the only traffic
 // that counts, 2 x layers x page bytes read and written per page, bound by HBM.
-// Measured: a fork of 31 sequences (free, fork and three small kernels) that moves
+// Measured: a fork of 32 sequences (free, fork and three small kernels) that moves
 // 0.27 GB: 49 us, 5.5 TB/s; a compaction that moves 0.46 GB: 81 us, 5.6 TB/s (of 6.5 TB/s
 // for a plain copy; 10 to 12 us are the deciding kernels and the launches).
 #include <algorithm>
